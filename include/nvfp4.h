@@ -121,14 +121,17 @@ enum {
     NVFP4_OP_GEMM = 2,     /* nvfp4_gemm                            */
     NVFP4_OP_MOE = 3,      /* nvfp4_moe_grouped_gemm                */
     NVFP4_OP_MOE_ROUTE = 4, /* nvfp4_moe_route / the staged GEMMs   */
-    NVFP4_OP_MX_MOE = 5     /* mx_moe_w4a8                          */
+    NVFP4_OP_MX_MOE = 5,    /* mx_moe_w4a8                          */
+    NVFP4_OP_KV_ATTENTION = 6 /* nvfp4_kv_attention                 */
 };
 
 /* Bytes of `ws` an operation needs.  Unused arguments may be 0:
  *   QUANTIZE: none.  REMAP: T = batch, H = rows, I = cols.
  *   GEMM: T = M (rows of A), H = K, I = N (rows of W); non-zero only for
  *         few-row shapes whose K is split over several workgroups.
- *   MOE, MOE_ROUTE: T tokens, k slots, E experts, H hidden, I intermediate. */
+ *   MOE, MOE_ROUTE: T tokens, k slots, E experts, H hidden, I intermediate.
+ *   KV_ATTENTION: T = n (query rows), k = q_heads, E = kv_heads, H = head_dim,
+ *         I = seqs. */
 size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 
 /*
@@ -245,6 +248,26 @@ nvfp4_status nvfp4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* W, void* C, i
  */
 nvfp4_status mxfp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t* fp8,
                             uint8_t* e8m0, void* stream);
+
+/*
+ * The residual's addition, the root-mean-square norm and the MXFP8 encode of
+ * its result in one pass (the activation operand of mx_gemm_w4a8):
+ *   r   = bf16(x + residual)                 (x without a residual)
+ *   inv = fp32(1 / sqrt(mean over the row of r^2 + eps)), the sum in fp64
+ *   y   = bf16((r * inv) * weight)           (fp32 steps; weight NULL: ones)
+ *   fp8, e8m0 = mxfp8_quantize(y)
+ * x, residual, sum, y: bf16 [rows, cols] with row strides ld_* (elements,
+ * multiples of 8, 16-byte aligned); weight: bf16 [cols].  Outputs, each
+ * optional: r to sum (may be x or residual itself with the same stride), y,
+ * and the pair fp8 [rows, cols] / e8m0 [rows, cols/32] (both or neither).  The
+ * result does not depend on how a row is split over threads.  cols % 32 == 0
+ * (else NVFP4_ERR_SHAPE) and cols <= 65536 on this build (else UNSUPPORTED);
+ * eps >= 0.  An all-zero row with eps = 0 gives unspecified output.
+ */
+nvfp4_status mxfp8_add_rmsnorm(const void* x_bf16, int64_t ld_x, const void* residual_bf16, int64_t ld_res,
+                               const void* weight_bf16, double eps, int64_t rows, int64_t cols, void* sum_bf16,
+                               int64_t ld_sum, void* y_bf16, int64_t ld_y, uint8_t* fp8, uint8_t* e8m0,
+                               void* stream);
 
 /*
  * MX-native W4A8 GEMM (page "DeepSeek-V4.1-Flash-NVFP4", section 二: MXFP4
@@ -464,6 +487,83 @@ nvfp4_status nvfp4_kv_quant(const void* k_bf16, const void* v_bf16, int64_t n, i
 nvfp4_status nvfp4_kv_dequant(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache,
                               int64_t heads, int64_t tok_begin, int64_t n, void* k_out,
                               void* v_out, int32_t dtype, void* stream);
+
+/*
+ * Write new tokens into a paged NVFP4 KV cache, with the rotation by position
+ * on the way.  The cache tensors are those of nvfp4_kv_quant (rows = (token,
+ * head), cols = head_dim D, static global); a page is a run of page_size
+ * tokens of them, so page p holds tokens [p * page_size, + page_size) and a
+ * token's slot is page * page_size + its place in the page.  For token i < n:
+ *   - q (bf16 [q_heads, D]) and k (bf16 [kv_heads, D]) are rotated by
+ *     positions[i]: with c, s = cos_sin[position, j], cos_sin[position,
+ *     rot_dim/2 + j] for pair j < rot_dim/2,
+ *       a' = bf16(a * c - b * s),  b' = bf16(b * c + a * s)
+ *     in fp32 without fused multiply-add, the pair (a, b) being elements
+ *     (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved != 0; elements
+ *     past rot_dim keep their value.  rot_dim = 0: no rotation.
+ *   - the rotated q goes to q_out; the rotated k and v are quantized with the
+ *     caches' globals and stored at token slots[i]: the bytes that
+ *     nvfp4_kv_quant would store for them.
+ * q, k, v may be slices of one projection's output: ld_* are token strides in
+ * elements (multiples of 8); heads are contiguous.  q may be NULL (then
+ * q_heads and q_out are not used), so may k or v.  q_out may be q itself with
+ * the same stride; no other buffers may overlap.  cos_sin: fp32 [max_pos,
+ * rot_dim], 16-byte aligned; positions int32 [n], slots int64 [n] on the
+ * device.  A negative slot stores nothing (padding); its q row is still
+ * rotated.  A slot past the cache or, on a token with a slot, a position
+ * outside [0, max_pos) raises the sticky NVFP4_ERR_RANGE and stores nothing;
+ * the q row of a token with such a position becomes zeros.  Slots that are not
+ * negative must differ from each other: of two tokens with the same slot,
+ * that slot's content is unspecified (other slots are not affected).
+ * D % 32 == 0, D <= 4096 and rot_dim % 32 == 0, rot_dim <= D on this build.
+ */
+nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, const void* k_bf16, int64_t ld_k,
+                             const void* v_bf16, int64_t ld_v, int32_t kv_heads, int64_t n, const int64_t* slots,
+                             const int32_t* positions, const float* cos_sin, int64_t max_pos, int32_t rot_dim,
+                             int32_t interleaved, void* q_out_bf16, int64_t ld_qout, const nvfp4_tensor* k_cache,
+                             const nvfp4_tensor* v_cache, void* stream);
+
+/*
+ * Attention over a paged NVFP4 KV cache, for `seqs` sequences of any lengths
+ * (grouped query heads: q head j reads KV head j / (q_heads / kv_heads)):
+ *   s[r, t] = scale * q[r] . k[t],  p = softmax_t over the tokens r sees,
+ *   out[r] = bf16(sum_t p[r, t] v[t]),  lse[r] = ln sum_t exp(s[r, t])
+ * with k, v the values (e2m1 * s) * G of the cache.  Sequence b has kv_lens[b]
+ * cached tokens; token t of it is in page block_table[b, t / page_size] of the
+ * cache, at place t % page_size.  Its query rows are cu_q[b] .. cu_q[b+1] - 1
+ * (cu_q: int32 [seqs + 1], cu_q[0] = 0, not decreasing), or row b alone when
+ * cu_q is NULL (then n == seqs).  They are the last tokens of the sequence: of
+ * m query rows, row i has position kv_lens[b] - m + i (write their keys with
+ * nvfp4_kv_append first).
+ *   causal != 0: row i sees the tokens up to its own position, with window > 0
+ *   only the last `window` of them (its own among them); causal == 0: every
+ *   cached token (window must be 0).
+ * A row that sees no token (an empty sequence, a position before 0) gets
+ * zeros and lse = -inf.  Rows behind the last sequence are not written.
+ *   q: bf16 [n, q_heads, D], token stride ld_q elements (a multiple of 8);
+ *   out: bf16, the same shape, token stride ld_out (not q: no overlap);
+ *   lse: fp32 [n, q_heads] or NULL;
+ *   max_q: the most query rows that a sequence has (it chooses the kernel; a
+ *   wrong one costs speed, not results); 1 when cu_q is NULL;
+ *   block_table: int32 [seqs, pages_per_seq], row stride ld_table.  Entries of
+ *   pages with no token that a row sees (past the sequence's length, before
+ *   the window) may hold anything;
+ *   ws: nvfp4_workspace_size(NVFP4_OP_KV_ATTENTION, n, q_heads, kv_heads, D,
+ *   seqs) bytes, 256-byte aligned (may be NULL if that is 0).
+ * Products are exact and summed in fp32 (q is held in f16 relative to its
+ * row's largest element, p in f16); results do not depend on anything but the
+ * arguments.  An entry that is not a page of the cache, a kv_lens[b] outside
+ * [0, pages_per_seq * page_size] or a cu_q that decreases or passes n raises
+ * the sticky NVFP4_ERR_RANGE: such a page's tokens are skipped, such a length
+ * is cut.  D is 64, 128 or 256 and page_size % 16 == 0 on this build (else
+ * NVFP4_ERR_UNSUPPORTED); scale finite and positive.
+ */
+nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads,
+                                const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,
+                                const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq,
+                                int32_t page_size, const int32_t* kv_lens, const int32_t* cu_q, int32_t seqs,
+                                int32_t max_q, float scale, int32_t causal, int32_t window, void* out_bf16,
+                                int64_t ld_out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Scale audit (page "Qwen3.8-Flash-Next-NVFP4", section 证据链: every block

@@ -11,6 +11,7 @@ scale per tensor -- 4.5 bits per element.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -23,7 +24,8 @@ __all__ = [
     "mxfp4_quantize", "mxfp4_to_nvfp4", "nvfp4_gemm", "nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_noalloc",
     "nvfp4_moe_route", "nvfp4_moe_gate_up", "nvfp4_moe_gate_up_q", "nvfp4_moe_down", "nvfp4_moe_combine",
     "nvfp4_gather_dequantize", "nvfp4_tile_scales", "nvfp4_gemm_w4a16", "nvfp4_moe_w4a16", "mxfp8_quantize", "mx_gemm_w4a8", "mx_moe_w4a8", "mx_moe_gate_up", "mx_moe_down",
-    "nvfp4_kv_quant", "nvfp4_kv_dequant", "nvfp4_audit_scales", "nvfp4_get_error", "nvfp4_set_checks",
+    "nvfp4_kv_quant", "nvfp4_kv_dequant", "nvfp4_kv_append", "nvfp4_kv_attention", "mxfp8_add_rmsnorm",
+    "nvfp4_audit_scales", "nvfp4_get_error", "nvfp4_set_checks",
     "nvfp4_recipe", "status_string",
 ]
 
@@ -469,6 +471,173 @@ def nvfp4_kv_dequant(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int, tok
     _check(_lib.load().nvfp4_kv_dequant(ctypes.byref(kc), ctypes.byref(vc), heads, tok_begin, n,
                                         _ptr(ko), _ptr(vo), code, _stream(dev)), "nvfp4_kv_dequant")
     return ko, vo
+
+
+def _on(device):
+    """Launches go to the operands' device: make it current if it is not."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _operand(t, what, dtype, dim, device):
+    """A device tensor argument of the given type and number of dimensions,
+    on `device`; the last dimension contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{what}: libnvfp4 operates on tensors of one device")
+    if t.dtype != dtype or t.dim() != dim:
+        raise ValueError(f"{what}: a {dim}-dimensional {dtype} tensor is expected")
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+
+
+def _heads(t, what, device):
+    """bf16 [n, heads, head_dim] with contiguous heads: the token stride."""
+    _operand(t, what, torch.bfloat16, 3, device)
+    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+        raise ValueError(f"{what}: heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, slots: torch.Tensor,
+                    k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, positions: torch.Tensor | None = None,
+                    cos_sin: torch.Tensor | None = None, interleaved: bool = False,
+                    q_out: torch.Tensor | None = None, heads: int | None = None) -> torch.Tensor | None:
+    """Rotate q and k (bf16 [n, heads, D], any token stride) by positions
+    (int32 [n]) with cos_sin (float32 [max_pos, rot_dim]: cosines, then
+    sines), quantize k and v into the caches at slots (int64 [n]; negative: not
+    stored).  Returns the rotated q (q_out, new if omitted; may be q).
+    Without cos_sin nothing is rotated.  heads: KV heads of the caches, needed
+    only when neither k nor v is given."""
+    device = k_cache.device
+    kv = k if k is not None else v
+    if kv is not None:
+        heads = kv.shape[1]
+    elif heads is None:
+        raise ValueError("heads is needed without k and v")
+    n = slots.numel()
+    ld = [0, 0, 0]
+    for j, (name, t) in enumerate((("q", q), ("k", k), ("v", v))):
+        if t is None:
+            continue
+        ld[j] = _heads(t, name, device)
+        if t.shape[0] != n or t.shape[2] != k_cache.cols or (j and t.shape[1] != heads):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit {n} slots and the cache")
+    _operand(slots, "slots", torch.int64, 1, device)
+    rot = max_pos = 0
+    if cos_sin is not None:
+        _operand(cos_sin, "cos_sin", torch.float32, 2, device)
+        if positions is None or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous and needs positions")
+        _operand(positions, "positions", torch.int32, 1, device)
+        if positions.numel() != n:
+            raise ValueError("positions: one per slot")
+        max_pos, rot = cos_sin.shape
+    ld_qo = 0
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+        ld_qo = _heads(q_out, "q_out", device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out: the shape of q is expected")
+    kc, vc = k_cache.c(), v_cache.c()
+    with _on(device):
+        st = _lib.load().nvfp4_kv_append(
+            _ptr(q), ld[0], 0 if q is None else q.shape[1], _ptr(k), ld[1], _ptr(v), ld[2], heads, n, _ptr(slots),
+            _ptr(positions), _ptr(cos_sin), max_pos, rot, int(interleaved), None if q is None else _ptr(q_out), ld_qo,
+            ctypes.byref(kc), ctypes.byref(vc), _stream(device))
+    _check(st, "nvfp4_kv_append")
+    return q_out if q is not None else None
+
+
+def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int,
+                       block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int,
+                       cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
+                       causal: bool = True, window: int = 0, return_lse: bool = False,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None):
+    """Attention of q (bf16 [n, q_heads, D]) over the paged NVFP4 caches of
+    `heads` KV heads: block_table int32 [seqs, pages], kv_lens int32 [seqs].
+    cu_q (int32 [seqs + 1]) gives each sequence's query rows, one row per
+    sequence without it; max_q the most rows a sequence has (n if omitted).
+    scale: 1 / sqrt(D) if omitted.  Returns out (bf16, the shape of q), or
+    (out, lse float32 [n, q_heads]) with return_lse or lse."""
+    device = q.device
+    ld_q = _heads(q, "q", device)
+    n, q_heads, D = q.shape
+    if k_cache.device != device or v_cache.device != device or k_cache.cols != D:
+        raise ValueError("q and the caches must be on one device, with one head_dim")
+    _operand(block_table, "block_table", torch.int32, 2, device)
+    _operand(kv_lens, "kv_lens", torch.int32, 1, device)
+    seqs, pages = block_table.shape
+    if kv_lens.numel() != seqs:
+        raise ValueError("kv_lens: one per row of block_table")
+    if cu_q is not None:
+        _operand(cu_q, "cu_q", torch.int32, 1, device)
+        if cu_q.numel() != seqs + 1:
+            raise ValueError("cu_q: seqs + 1 entries")
+    if max_q is None:
+        max_q = 1 if cu_q is None else n
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+    ld_out = _heads(out, "out", device)
+    if out.shape != q.shape:
+        raise ValueError("out: the shape of q is expected")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((n, q_heads), dtype=torch.float32, device=device)
+    else:
+        _operand(lse, "lse", torch.float32, 2, device)
+        if lse.shape != (n, q_heads) or not lse.is_contiguous():
+            raise ValueError("lse: a contiguous [n, q_heads] tensor is expected")
+    lib = _lib.load()
+    if ws is None:
+        need = lib.nvfp4_workspace_size(_lib.OP_KV_ATTENTION, n, q_heads, heads, D, seqs)
+        ws = _workspace(need, device) if need else None
+    kc, vc = k_cache.c(), v_cache.c()
+    with _on(device):
+        st = lib.nvfp4_kv_attention(
+            _ptr(q), ld_q, n, q_heads, ctypes.byref(kc), ctypes.byref(vc), heads, _ptr(block_table),
+            max(block_table.stride(0), pages), pages, page_size, _ptr(kv_lens), _ptr(cu_q), seqs, max_q,
+            D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), ld_out, _ptr(lse), _ptr(ws),
+            0 if ws is None else ws.numel(), _stream(device))
+    _check(st, "nvfp4_kv_attention")
+    return out if lse is None else (out, lse)
+
+
+def mxfp8_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor | None, eps: float = 1e-6,
+                      want_y: bool = False, want_fp8: bool = True, sum_out: torch.Tensor | None = None):
+    """RMS norm of r = x + residual (bf16 [rows, cols], any row stride) with its
+    MXFP8 encode: (r, y, fp8 uint8 [rows, cols], e8m0 uint8 [rows, cols/32]).
+    r is x itself without a residual and is written to sum_out (new if
+    omitted; may be x or residual) with one; y (bf16) and the MXFP8 pair are
+    None unless wanted."""
+    device = x.device
+    _operand(x, "x", torch.bfloat16, 2, device)
+    rows, cols = x.shape
+    ld = [0, 0, 0]
+    for j, (name, t) in enumerate((("x", x), ("residual", residual), ("sum_out", sum_out))):
+        if t is None:
+            continue
+        _operand(t, name, torch.bfloat16, 2, device)
+        if t.shape != x.shape:
+            raise ValueError(f"{name}: the shape of x is expected")
+        ld[j] = t.stride(0) if rows > 1 else cols
+    if weight is not None:
+        _operand(weight, "weight", torch.bfloat16, 1, device)
+        if weight.numel() != cols:
+            raise ValueError("weight: one per column")
+    total = x if residual is None and sum_out is None else sum_out
+    if total is None:
+        total = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        ld[2] = cols
+    y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device) if want_y else None
+    fp8 = torch.empty((rows, cols), dtype=torch.uint8, device=device) if want_fp8 else None
+    e8 = torch.empty((rows, cols // 32), dtype=torch.uint8, device=device) if want_fp8 else None
+    with _on(device):
+        st = _lib.load().mxfp8_add_rmsnorm(
+            _ptr(x), ld[0], _ptr(residual), ld[1], _ptr(weight), eps, rows, cols, None if total is x and residual is None else _ptr(total),
+            ld[2], _ptr(y), cols, _ptr(fp8), _ptr(e8), _stream(device))
+    _check(st, "mxfp8_add_rmsnorm")
+    return total, y, fp8, e8
 
 
 def nvfp4_audit_scales(t: NVFP4Tensor) -> torch.Tensor:

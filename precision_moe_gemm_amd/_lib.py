@@ -19,7 +19,7 @@ _lib = None
 
 OK, INVALID_ARG, SHAPE, RANGE, WORKSPACE, DEVICE, UNSUPPORTED, DATA = range(8)
 F32, BF16 = 0, 1
-OP_QUANTIZE, OP_REMAP, OP_GEMM, OP_MOE, OP_MOE_ROUTE, OP_MX_MOE = range(6)
+OP_QUANTIZE, OP_REMAP, OP_GEMM, OP_MOE, OP_MOE_ROUTE, OP_MX_MOE, OP_KV_ATTENTION = range(7)
 
 
 class NVFP4TensorC(ctypes.Structure):
@@ -72,6 +72,10 @@ SIGNATURES = {
     "nvfp4_moe_combine": (ST, [P, P, P, I64, I32, I64, P, P]),
     "nvfp4_kv_quant": (ST, [P, P, I64, I64, I64, TP, TP, P]),
     "nvfp4_kv_dequant": (ST, [TP, TP, I64, I64, I64, P, P, ctypes.c_int, P]),
+    "nvfp4_kv_append": (ST, [P, I64, I32, P, I64, P, I64, I32, I64, P, P, P, I64, I32, I32, P, I64, TP, TP, P]),
+    "nvfp4_kv_attention": (ST, [P, I64, I64, I32, TP, TP, I32, P, I64, I32, I32, P, P, I32, I32, ctypes.c_float, I32, I32,
+                                P, I64, P, P, SZ, P]),
+    "mxfp8_add_rmsnorm": (ST, [P, I64, P, I64, P, ctypes.c_double, I64, I64, P, I64, P, I64, P, P, P]),
     "nvfp4_audit_scales": (ST, [TP, P, P]),
     "nvfp4_get_error": (ST, [P]),
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),

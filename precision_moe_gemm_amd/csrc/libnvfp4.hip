@@ -9,11 +9,14 @@
 #include <cstring>
 #include <initializer_list>
 
+#include "attn.h"
 #include "common.h"
 #include "gemm.h"
+#include "kvcache.h"
 #include "moe.h"
 #include "mx.h"
 #include "mx8.h"
+#include "norm.h"
 #include "quant.h"
 
 #ifndef NVFP4_BUILD_STAMP
@@ -192,6 +195,44 @@ nvfp4_status quantize_impl(const void* x, int64_t rows, int64_t cols, int64_t ld
         return launch_status();
     }
     return launch_quantize(a, 1, st);
+}
+
+// ---------------------------------------------------------------- attention
+// KV append: enough row slices per token that about 2048 workgroups run.
+void launch_kv_append(const AppendArgs& a, hipStream_t st)
+{
+    const int rows = a.heads[0] + a.heads[1] + a.heads[2];
+    const int per = 256 / (a.cpr / 2);
+    const unsigned gy = (unsigned)std::min<int64_t>(a.n, 65535);
+    const int64_t gx = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, a.n), ceil_div(rows, per)));
+    kv_append_kernel<<<dim3((unsigned)gx, gy), 256, 0, st>>>(a);
+}
+
+template <int D>
+nvfp4_status launch_attention(const AttnArgs& a, hipStream_t st)
+{
+    const int64_t items = a.n * a.group / 16 + a.seqs;
+    if (items > 0x7FFFFFFF)
+        return NVFP4_ERR_UNSUPPORTED;
+    attn_rows_kernel<D, 1><<<dim3((unsigned)items, a.kv_heads / a.head_lanes), kAttnThreads, 0, st>>>(a);
+    return launch_status();
+}
+
+// RMS norm: 1024-thread workgroups, up to 8 chunks of 8 elements per thread.
+constexpr int64_t kNormMaxCols = 65536;
+void launch_add_rmsnorm(const NormArgs& a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
+    const int threads = (int)std::min<int64_t>(1024, ceil_div(a.chunks, 64) * 64);
+    const int64_t per = ceil_div(a.chunks, threads);
+    if (per <= 1)
+        add_rmsnorm_kernel<1><<<grid, threads, 0, st>>>(a);
+    else if (per <= 2)
+        add_rmsnorm_kernel<2><<<grid, threads, 0, st>>>(a);
+    else if (per <= 4)
+        add_rmsnorm_kernel<4><<<grid, threads, 0, st>>>(a);
+    else
+        add_rmsnorm_kernel<8><<<grid, threads, 0, st>>>(a);
 }
 
 // ---------------------------------------------------------------- GEMM
@@ -949,6 +990,11 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         if (T < 0 || k < 1 || E < 1)
             return 0;
         return mx_moe_layout(T, k, E, H, I).end;
+    case NVFP4_OP_KV_ATTENTION:
+        // T query rows, k query heads, E KV heads, H = head_dim, I = sequences
+        if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
+            return 0;
+        return 0;
     }
     return 0;
 }
@@ -1966,6 +2012,209 @@ nvfp4_status nvfp4_audit_scales(const nvfp4_tensor* t, int64_t* counts, void* st
         audit_kernel<<<stream_grid(n, 1024), kQuantThreads, 0, S(stream)>>>(t->scales, n,
                                                                              (unsigned long long*)counts);
     return launch_status();
+}
+
+nvfp4_status nvfp4_kv_append(const void* q, int64_t ld_q, int32_t q_heads, const void* k, int64_t ld_k, const void* v,
+                             int64_t ld_v, int32_t kv_heads, int64_t n, const int64_t* slots,
+                             const int32_t* positions, const float* cos_sin, int64_t max_pos, int32_t rot_dim,
+                             int32_t interleaved, void* q_out, int64_t ld_qout, const nvfp4_tensor* k_cache,
+                             const nvfp4_tensor* v_cache, void* stream)
+{
+    const nvfp4_tensor* cache[2] = {k_cache, v_cache};
+    if (n < 0 || kv_heads < 1 || (q && q_heads < 1))
+        return NVFP4_ERR_SHAPE;
+    for (int j = 0; j < 2; j++) {
+        nvfp4_status s = check_tensor(cache[j]);
+        if (s != NVFP4_OK)
+            return s;
+        if (cache[j]->batch != 1 || cache[j]->rows % kv_heads != 0)
+            return NVFP4_ERR_SHAPE;
+    }
+    const int64_t D = k_cache->cols;
+    if (v_cache->cols != D || v_cache->rows != k_cache->rows || rot_dim < 0 || rot_dim > D)
+        return NVFP4_ERR_SHAPE;
+    if (n == 0 || (!q && !k && !v))
+        return NVFP4_OK;
+    if (D == 0 || D % 32 != 0 || D > 4096 || rot_dim % 32 != 0)
+        return NVFP4_ERR_UNSUPPORTED;
+    const int64_t heads[3] = {q ? q_heads : 0, k ? kv_heads : 0, v ? kv_heads : 0};
+    const void* src[4] = {q, k, v, q ? q_out : nullptr};
+    const int64_t ld[4] = {ld_q, ld_k, ld_v, ld_qout};
+    for (int j = 0; j < 4; j++) {
+        if (!src[j])
+            continue;
+        if (!aligned(src[j], 16))
+            return NVFP4_ERR_INVALID_ARG;
+        if (ld[j] < heads[j % 3] * D || ld[j] % 8 != 0)
+            return NVFP4_ERR_SHAPE;
+    }
+    if ((q && !q_out) || !slots || !aligned(slots, 8))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!positions || !aligned(positions, 4) || !cos_sin || !aligned(cos_sin, 16)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rot_dim > 0 && max_pos < 1)
+        return NVFP4_ERR_SHAPE;
+    if (heads[0] + 2 * (int64_t)kv_heads > 65536)
+        return NVFP4_ERR_UNSUPPORTED;
+    AppendArgs a{};
+    for (int j = 0; j < 3; j++) {
+        a.x[j] = (const uint16_t*)src[j];
+        a.ld[j] = ld[j];
+        a.heads[j] = (int)heads[j];
+    }
+    a.q_out = (uint16_t*)q_out;
+    a.ld_qout = ld_qout;
+    for (int j = 0; j < 2; j++) {
+        a.packed[j] = (uint32_t*)cache[j]->packed;
+        a.scales[j] = cache[j]->scales;
+        a.global[j] = cache[j]->global;
+    }
+    a.slots = slots;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.max_pos = max_pos;
+    a.tokens = k_cache->rows / kv_heads;
+    a.n = n;
+    a.cpr = (int)(D / 8);
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    launch_kv_append(a, S(stream));
+    nvfp4_status s = launch_status();
+    if (s == NVFP4_OK && checks_on()) {
+        for (int j = 0; j < 3; j++)
+            if (src[j])
+                check_bf16(src[j], n, heads[j] * D, ld[j], S(stream));
+        check_globals(k_cache->global, 1, S(stream));
+        check_globals(v_cache->global, 1, S(stream));
+        s = launch_status();
+    }
+    return s;
+}
+
+nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
+                                const nvfp4_tensor* v_cache, int32_t kv_heads, const int32_t* block_table,
+                                int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                                const int32_t* cu_q, int32_t seqs, int32_t max_q, float scale, int32_t causal,
+                                int32_t window, void* out, int64_t ld_out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream)
+{
+    const nvfp4_tensor* cache[2] = {k_cache, v_cache};
+    if (n < 0 || seqs < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || pages_per_seq < 0 ||
+        ld_table < pages_per_seq || page_size < 1 || max_q < 0)
+        return NVFP4_ERR_SHAPE;
+    for (int j = 0; j < 2; j++) {
+        nvfp4_status s = check_tensor(cache[j]);
+        if (s != NVFP4_OK)
+            return s;
+        if (cache[j]->batch != 1 || cache[j]->rows % kv_heads != 0)
+            return NVFP4_ERR_SHAPE;
+    }
+    const int64_t D = k_cache->cols;
+    if (v_cache->cols != D || v_cache->rows != k_cache->rows || (!cu_q && n != seqs))
+        return NVFP4_ERR_SHAPE;
+    if (!(scale > 0.0f) || scale > 3.0e38f || window < 0 || (window > 0 && !causal))
+        return NVFP4_ERR_INVALID_ARG;
+    if (n == 0 || seqs == 0)
+        return NVFP4_OK;
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 != 0)
+        return NVFP4_ERR_UNSUPPORTED;
+    const int64_t num_pages = k_cache->rows / kv_heads / page_size;
+    if ((int64_t)pages_per_seq * page_size > 0x7FFFFF00 || n * q_heads > 0x7FFFFF00 || kv_heads > 4 * 65535)
+        return NVFP4_ERR_UNSUPPORTED;
+    if (ld_q < q_heads * D || ld_q % 8 != 0 || ld_out < q_heads * D || ld_out % 8 != 0 ||
+        (pages_per_seq > 0 && num_pages < 1))
+        return NVFP4_ERR_SHAPE;
+    if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
+        !aligned(lse, 4) || (pages_per_seq > 0 && !block_table) || !aligned(block_table, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_ATTENTION, n, q_heads, kv_heads, D, seqs);
+    if (need > 0 && (!ws || !aligned(ws, 256)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < need)
+        return NVFP4_ERR_WORKSPACE;
+    AttnArgs a{};
+    a.q = (const uint16_t*)q;
+    a.ld_q = ld_q;
+    a.k_packed = k_cache->packed;
+    a.k_scales = k_cache->scales;
+    a.v_packed = v_cache->packed;
+    a.v_scales = v_cache->scales;
+    a.k_global = k_cache->global;
+    a.v_global = v_cache->global;
+    a.cu_q = cu_q;
+    a.kv_lens = kv_lens;
+    a.table = block_table;
+    a.ld_table = ld_table;
+    a.num_pages = num_pages;
+    a.n = n;
+    a.seqs = seqs;
+    a.pages = pages_per_seq;
+    a.page = page_size;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.scale_log2 = scale * 1.44269504089f;
+    a.causal = causal != 0;
+    a.window = window;
+    a.out = (uint16_t*)out;
+    a.ld_out = ld_out;
+    a.lse = lse;
+    a.head_lanes = kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1);
+    nvfp4_status s = D == 64 ? launch_attention<64>(a, S(stream))
+                             : (D == 128 ? launch_attention<128>(a, S(stream)) : launch_attention<256>(a, S(stream)));
+    if (s == NVFP4_OK && checks_on()) {
+        check_bf16(q, n, q_heads * D, ld_q, S(stream));
+        s = check_tensors_data({k_cache, v_cache}, S(stream));
+    }
+    return s;
+}
+
+nvfp4_status mxfp8_add_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, const void* weight,
+                               double eps, int64_t rows, int64_t cols, void* sum, int64_t ld_sum, void* y, int64_t ld_y,
+                               uint8_t* fp8, uint8_t* e8m0, void* stream)
+{
+    if (rows < 0 || cols < 0 || cols % 32 != 0)
+        return NVFP4_ERR_SHAPE;
+    const void* mat[4] = {x, residual, sum, y};
+    const int64_t ld[4] = {ld_x, ld_res, ld_sum, ld_y};
+    for (int j = 0; j < 4; j++)
+        if ((mat[j] || j == 0) && (ld[j] < cols || ld[j] % 8 != 0))
+            return NVFP4_ERR_SHAPE;
+    if (!(eps >= 0.0) || eps > 1.0e300 || (fp8 == nullptr) != (e8m0 == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return NVFP4_OK;
+    if (cols > kNormMaxCols)
+        return NVFP4_ERR_UNSUPPORTED;
+    if (!x || !aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) ||
+        !aligned(y, 16) || !aligned(fp8, 16))
+        return NVFP4_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.x = (const u32x4*)x;
+    a.residual = (const u32x4*)residual;
+    a.weight = (const u32x4*)weight;
+    a.sum = (u32x4*)sum;
+    a.y = (u32x4*)y;
+    a.fp8 = (u32x2*)fp8;
+    a.e8m0 = e8m0;
+    a.rows = rows;
+    a.ld_x = ld_x / 8;
+    a.ld_res = ld_res / 8;
+    a.ld_sum = ld_sum / 8;
+    a.ld_y = ld_y / 8;
+    a.chunks = (int)(cols / 8);
+    a.cols = (double)cols;
+    a.eps = eps;
+    launch_add_rmsnorm(a, S(stream));
+    nvfp4_status s = launch_status();
+    if (s == NVFP4_OK && checks_on()) {
+        check_bf16(x, rows, cols, ld_x, S(stream));
+        if (residual)
+            check_bf16(residual, rows, cols, ld_res, S(stream));
+        if (weight)
+            check_bf16(weight, 1, cols, cols, S(stream));
+        s = launch_status();
+    }
+    return s;
 }
 
 }  // extern "C"

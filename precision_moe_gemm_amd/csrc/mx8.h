@@ -58,6 +58,29 @@ NVFP4_DEV int mx8_exponent(uint32_t amax_bits16)
     return e < -127 ? -127 : (e > 127 ? 127 : e);
 }
 
+// Eight bf16 values (one u32x4) times 2^-e, e in [-127, 127], as E4M3 bytes.
+NVFP4_DEV u32x2 mx8_encode8(u32x4 v, int e)
+{
+    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);  // 2^-e (e in [-127, 127])
+    // 2^-e for e = -127 is 2^127: representable; e = 127 gives 2^-127, a
+    // subnormal fp32 whose exponent field is 0: build it from two factors
+    const float inv_lo = e == 127 ? 0x1p-64f : 1.0f;
+    const float inv_hi = e == 127 ? 0x1p-63f : inv;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t q[2];
+#pragma unroll
+    for (int hh = 0; hh < 2; hh++) {
+        const float f0 = __builtin_bit_cast(float, w[2 * hh] << 16) * inv_hi * inv_lo;
+        const float f1 = __builtin_bit_cast(float, w[2 * hh] & 0xFFFF0000u) * inv_hi * inv_lo;
+        const float f2 = __builtin_bit_cast(float, w[2 * hh + 1] << 16) * inv_hi * inv_lo;
+        const float f3 = __builtin_bit_cast(float, w[2 * hh + 1] & 0xFFFF0000u) * inv_hi * inv_lo;
+        uint32_t pk = __builtin_amdgcn_cvt_pk_fp8_f32(f0, f1, 0, false);
+        pk = __builtin_amdgcn_cvt_pk_fp8_f32(f2, f3, pk, true);
+        q[hh] = pk;
+    }
+    return (u32x2){q[0], q[1]};
+}
+
 // Work item = 8 elements (one 16-byte bf16 chunk, one 8-byte fp8 output):
 // consecutive lanes take consecutive chunks, so loads and stores are whole
 // lines per instruction, and the 4 lanes of a 32-element block share its
@@ -93,25 +116,9 @@ mxfp8_encode_kernel(const u32x4* __restrict__ x, int64_t rows, int64_t blocks_pe
             o = (uint32_t)__shfl_xor((int)am, 2, 64);
             am = am > o ? am : o;
             const int e = mx8_exponent(am);
-            const float inv = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);  // 2^-e (e in [-127, 127])
-            // 2^-e for e = -127 is 2^127: representable; e = 127 gives 2^-127, a
-            // subnormal fp32 whose exponent field is 0: build it from two factors
-            const float inv_lo = e == 127 ? 0x1p-64f : 1.0f;
-            const float inv_hi = e == 127 ? 0x1p-63f : inv;
-            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            uint32_t q[2];
-#pragma unroll
-            for (int hh = 0; hh < 2; hh++) {
-                const float f0 = __builtin_bit_cast(float, w[2 * hh] << 16) * inv_hi * inv_lo;
-                const float f1 = __builtin_bit_cast(float, w[2 * hh] & 0xFFFF0000u) * inv_hi * inv_lo;
-                const float f2 = __builtin_bit_cast(float, w[2 * hh + 1] << 16) * inv_hi * inv_lo;
-                const float f3 = __builtin_bit_cast(float, w[2 * hh + 1] & 0xFFFF0000u) * inv_hi * inv_lo;
-                uint32_t pk = __builtin_amdgcn_cvt_pk_fp8_f32(f0, f1, 0, false);
-                pk = __builtin_amdgcn_cvt_pk_fp8_f32(f2, f3, pk, true);
-                q[hh] = pk;
-            }
+            const u32x2 q = mx8_encode8(v[u], e);
             if (h < nq) {
-                out[h] = (u32x2){q[0], q[1]};
+                out[h] = q;
                 if ((h & 3) == 0)
                     e8m0[h >> 2] = (uint8_t)(e + 127);
             }
