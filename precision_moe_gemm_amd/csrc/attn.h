@@ -57,6 +57,8 @@ struct AttnArgs {
     int64_t ld_out;
     float* lse;              // [n, heads] or null
     int head_lanes;          // KV heads a workgroup holds side by side (1, 2 or 4)
+    int workers;             // shares that the tokens are cut into (at most)
+    float* partial;          // what shares leave of sequences that they hold a part of
 };
 
 constexpr int kAttnThreads = 256;
@@ -108,57 +110,78 @@ NVFP4_DEV void attn_limits(const AttnArgs& a, const AttnSeq& s, int i, int* star
     *start = b < 0 ? 0 : b;
 }
 
-// The sequence that holds item x when sequence b has count(b) items, the
-// item's number in it and the number of all items.  All threads of a
-// workgroup of kAttnThreads call it; every thread sums a contiguous share of
-// the sequences.
+// Work of a row kernel is counted in units: sequence b has tiles(b) tiles of
+// rows and units(b) steps of tokens for each of them (at least one, so that
+// rows that see nothing are written too).  The sequence that holds unit x (or
+// tile x, by_tile), the number of that unit (tile) in the sequence, the units
+// before the sequence and the units of all sequences.  All threads of the
+// workgroup call it; every thread sums a contiguous run of sequences.
+struct AttnCount {
+    int64_t tiles, units;
+};
 struct AttnFound {
-    int64_t total, local;
+    int64_t local, before, total, all_tiles;
     int seq;
 };
 
+constexpr int kAttnFoundLds = 2 * 16 + 3;
+
 template <class Count>
-NVFP4_DEV AttnFound attn_locate(int seqs, int64_t x, int64_t* lds, Count count)
+NVFP4_DEV AttnFound attn_locate(int seqs, int64_t x, bool by_tile, int64_t* lds, Count count)
 {
-    const int per = (seqs + kAttnThreads - 1) / kAttnThreads;
+    const int nt = blockDim.x, waves = nt >> 6, wave = threadIdx.x >> 6;
+    const int per = (seqs + nt - 1) / nt;
     const int b0 = threadIdx.x * per, b1 = b0 + per < seqs ? b0 + per : seqs;
-    int64_t mine = 0;
-    for (int b = b0; b < b1; b++)
-        mine += count(b);
-    int64_t up = mine;  // inclusive sum over the wave's lanes
+    AttnCount mine = {0, 0};
+    for (int b = b0; b < b1; b++) {
+        const AttnCount c = count(b);
+        mine.tiles += c.tiles;
+        mine.units += c.tiles * c.units;
+    }
+    AttnCount up = mine;  // inclusive sums over the wave's lanes
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(up, off, 64);
-        up += (int)(threadIdx.x & 63) >= off ? o : 0;
+        const int64_t a = __shfl_up(up.tiles, off, 64), u = __shfl_up(up.units, off, 64);
+        const bool in = (int)(threadIdx.x & 63) >= off;
+        up.tiles += in ? a : 0;
+        up.units += in ? u : 0;
+    }
+    if ((threadIdx.x & 63) == 63) {
+        lds[2 * wave] = up.tiles;
+        lds[2 * wave + 1] = up.units;
     }
     __syncthreads();
-    if ((threadIdx.x & 63) == 63)
-        lds[threadIdx.x >> 6] = up;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnThreads / 64; w++) {
-        before += w < (int)(threadIdx.x >> 6) ? lds[w] : 0;
-        total += lds[w];
+    AttnCount before = {0, 0}, total = {0, 0};
+    for (int w = 0; w < waves; w++) {
+        before.tiles += w < wave ? lds[2 * w] : 0;
+        before.units += w < wave ? lds[2 * w + 1] : 0;
+        total.tiles += lds[2 * w];
+        total.units += lds[2 * w + 1];
     }
-    before += up - mine;
-    if (x >= before && x < before + mine) {
-        int64_t rest = x - before;
+    before.tiles += up.tiles - mine.tiles;
+    before.units += up.units - mine.units;
+    int64_t rest = x - (by_tile ? before.tiles : before.units);
+    if (rest >= 0 && rest < (by_tile ? mine.tiles : mine.units)) {
         int b = b0;
-        for (; b < b1 - 1; b++) {
-            const int64_t c = count(b);
-            if (rest < c)
+        for (; b < b1; b++) {
+            const AttnCount c = count(b);
+            const int64_t size = by_tile ? c.tiles : c.tiles * c.units;
+            if (rest < size)
                 break;
-            rest -= c;
+            rest -= size;
+            before.units += c.tiles * c.units;
         }
-        lds[4] = rest;
-        lds[5] = b;
+        lds[32] = rest;
+        lds[33] = before.units;
+        lds[34] = b;
     }
     __syncthreads();
     AttnFound f;
-    f.total = total;
-    f.local = lds[4];
-    f.seq = (int)lds[5];
+    f.local = lds[32];
+    f.before = lds[33];
+    f.total = total.units;
+    f.all_tiles = total.tiles;
+    f.seq = (int)lds[34];
     return f;
 }
 
@@ -277,13 +300,15 @@ struct AttnWave {
         }
     }
 
-    // the 16 tokens of half `half` of a step: they lie in one page
-    NVFP4_DEV void load_half(const AttnArgs& a, AttnRaw<D>& raw, int half, int h, int64_t tok)
+    // the 16 tokens of half `half` of a step: they lie in one page.  The first
+    // token's row is the same for all lanes, so it goes into the scalar base
+    // of the loads and the lane's part is 32 bits.
+    NVFP4_DEV void load_half(const AttnArgs& a, AttnRaw<D>& raw, int half, int h, int64_t tok) const
     {
         const int64_t row = tok * a.kv_heads + h;  // the first token's cache row
-        const int stride = a.kv_heads;
-        const uint8_t* kc = a.k_packed + row * (D / 2) + (lane_n() * stride) * (D / 2) + lane_g() * (D / 8);
-        const uint8_t* ks = a.k_scales + row * (D / 16) + (lane_n() * stride) * (D / 16) + lane_g() * (D / 64);
+        const uint32_t stride = a.kv_heads;
+        const uint8_t* kc = a.k_packed + row * (D / 2) + (uint32_t)(lane_n() * stride * (D / 2) + lane_g() * (D / 8));
+        const uint8_t* ks = a.k_scales + row * (D / 16) + (uint32_t)(lane_n() * stride * (D / 16) + lane_g() * (D / 64));
         if constexpr (D == 64) {
             const u32x2 w = *(const u32x2*)kc;
             raw.kc[half][0] = w.x;
@@ -302,11 +327,11 @@ struct AttnWave {
             else
                 raw.ks[half] = *(const uint32_t*)ks;
         }
-        const uint8_t* vc = a.v_packed + row * (D / 2) + (4 * lane_g() * stride) * (D / 2) + lane_n() * (D / 32);
-        const uint8_t* vs = a.v_scales + row * (D / 16) + (4 * lane_g() * stride) * (D / 16) + lane_n() * D / 256;
+        const uint32_t vo = 4 * lane_g() * stride * (D / 2) + lane_n() * (D / 32);
+        const uint32_t so = 4 * lane_g() * stride * (D / 16) + lane_n() * D / 256;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const uint8_t* p = vc + j * stride * (D / 2);
+            const uint8_t* p = a.v_packed + (row + j * (int64_t)stride) * (D / 2) + vo;
             if constexpr (D == 64) {
                 raw.vc[4 * half + j][0] = *(const uint16_t*)p;
             } else if constexpr (D == 128) {
@@ -316,7 +341,7 @@ struct AttnWave {
                 raw.vc[4 * half + j][0] = w.x;
                 raw.vc[4 * half + j][1] = w.y;
             }
-            raw.vs[4 * half + j] = vs[j * stride * (D / 16)];
+            raw.vs[4 * half + j] = a.v_scales[(row + j * (int64_t)stride) * (D / 16) + so];
         }
     }
 
@@ -417,8 +442,25 @@ struct AttnWave {
         }
     }
 
+    // the step at token t0 + 32 k of a walk (the last one again past the end)
+    NVFP4_DEV void load(const AttnArgs& a, AttnPages& pages, AttnRaw<D>& raw, bool (&ok)[2], int h, int t) const
+    {
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            int i = (t + 16 * half) / a.page;
+            const int off = t + 16 * half - i * a.page;
+            i = i < pages.last ? i : pages.last;  // past the end: any page, masked
+            const int page = pages.get(a, i);
+            ok[half] = page >= 0;
+            load_half(a, raw, half, h, (int64_t)(page < 0 ? 0 : page) * a.page + off);
+        }
+    }
+
     // tokens [t0, t1) (t0 a multiple of 32); any: the first token that some
-    // row sees; [lo, hi): the tokens that every row sees
+    // row sees; [lo, hi): the tokens that every row sees.  Each step's data is
+    // requested while the step before it is computed; the requests are
+    // unconditional (past the end the last step's, which is in the cache), so
+    // that the compiler can count them and wait for the older step only.
     NVFP4_DEV void walk(const AttnArgs& a, const int32_t* table_row, int h, int t0, int t1, int any, int lo, int hi)
     {
         if (t0 >= t1)
@@ -427,25 +469,24 @@ struct AttnWave {
         pages.row = table_row;
         pages.last = (t1 - 1) / a.page;
         pages.needed = any / a.page;
-        int idx = t0 / a.page, off = t0 - idx * a.page;
-        pages.fill(a, idx);
-        for (int t = t0; t < t1; t += kAttnStep) {
-            AttnRaw<D> raw;
-            bool ok[2];
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                const int i = idx < pages.last ? idx : pages.last;  // past the end: any page, masked
-                const int page = pages.get(a, i);
-                ok[half] = page >= 0;
-                load_half(a, raw, half, h, (int64_t)(page < 0 ? 0 : page) * a.page + off);
-                off += 16;
-                if (off == a.page) {
-                    off = 0;
-                    idx++;
-                }
-            }
-            step(raw, t, ok[0] && ok[1] && t >= lo && t + kAttnStep <= hi, ok);
+        pages.fill(a, t0 / a.page);
+        const int end = t0 + (t1 - t0 - 1) / kAttnStep * kAttnStep;  // the last step
+        AttnRaw<D> x, y;
+        bool okx[2], oky[2];
+        load(a, pages, x, okx, h, t0);
+        for (int t = t0; t <= end; t += 2 * kAttnStep) {
+            const int u = t + kAttnStep, v = u + kAttnStep;
+            load(a, pages, y, oky, h, u < end ? u : end);
+            step(x, t, okx[0] && okx[1] && t >= lo && u <= hi, okx);
+            load(a, pages, x, okx, h, v < end ? v : end);
+            if (u <= end)
+                step(y, u, oky[0] && oky[1] && u >= lo && v <= hi, oky);
         }
+    }
+
+    // the sums of the lane groups
+    NVFP4_DEV void close()
+    {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             l[t] += __shfl_xor(l[t], 16, 64);
@@ -522,40 +563,213 @@ NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT>& w, const At
     }
 }
 
-// One workgroup: 16 NT query rows of one sequence for head_lanes KV heads
-// (blockIdx.y), each wave one of the heads and a share of the tokens.
+// Floats that one wave leaves of a part of its tokens: m, l and o of its 64
+// lanes, 16 NT query rows.
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads)
+constexpr int attn_part() { return (D / 4 + 2) * NT * 64; }
+
+// The shares: the units of all sequences in a row, cut into equal runs, at
+// least `least` units each.  Share w holds units [w T / W, (w + 1) T / W).
+NVFP4_DEV int64_t attn_shares(const AttnArgs& a, int64_t total, int least)
+{
+    const int64_t most = (total + least - 1) / least;
+    return most < a.workers ? most : a.workers;
+}
+
+template <int D, int NT>
+NVFP4_DEV AttnCount attn_count(const AttnArgs& a, int b)
+{
+    const AttnSeq s = attn_seq(a, b);
+    int lo0, hi0, lo1, hi1;
+    attn_limits(a, s, 0, &lo0, &hi0);
+    attn_limits(a, s, s.nq > 0 ? s.nq - 1 : 0, &lo1, &hi1);
+    const int t0 = lo0 & ~(kAttnStep - 1);
+    AttnCount c;
+    c.tiles = ((int64_t)s.nq * a.group + 16 * NT - 1) / (16 * NT);
+    c.units = hi1 > t0 ? (hi1 - t0 + kAttnStep - 1) / kAttnStep : 1;
+    return c;
+}
+
+// Few query rows per sequence (decode, drafts): the time is the K and V
+// bytes' way from HBM.  The tokens of all sequences are cut into equal shares,
+// one per resident workgroup, so that long and short sequences load the chip
+// alike; a share that holds a whole tile of rows writes its output, one that
+// holds a part leaves (m, l, o) for attn_combine_kernel, in slot 1 if it holds
+// the tile's first unit, else in slot 0 (a share has at most one of each).
+// A workgroup holds head_lanes KV heads side by side, which lie next to each
+// other in memory, and (waves / head_lanes) runs of the tokens.
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1)))
 attn_rows_kernel(AttnArgs a)
 {
-    __shared__ int64_t found[6];
-    __shared__ float buf[2 * (D / 4 + 2) * NT * 64];
+    __shared__ int64_t found[kAttnFoundLds];
+    __shared__ float buf[2 * attn_part<D, NT>()];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int hl = a.head_lanes, tls = (kAttnThreads / 64) / hl;
-    const int h = blockIdx.y * hl + wave % hl, tl = wave / hl;
-    const AttnFound f = attn_locate(a.seqs, blockIdx.x, found, [&](int b) {
-        const AttnSeq s = attn_seq(a, b);
-        return ((int64_t)s.nq * a.group + 16 * NT - 1) / (16 * NT);
-    });
-    if (blockIdx.x >= f.total)
+    // workgroups go to the 8 XCDs in turn: the head blocks of one share go to
+    // the same one, whose L2 then holds the lines that they share
+    const int blocks = a.kv_heads / hl;
+    const int hb = blockIdx.x / 8 % blocks, w = blockIdx.x / (8 * blocks) * 8 + blockIdx.x % 8;
+    const int h = hb * hl + wave % hl, tl = wave / hl;
+    auto count = [&](int b) { return attn_count<D, NT>(a, b); };
+    // (the total first: the share's bounds need it)
+    AttnFound f = attn_locate(a.seqs, 0, false, found, count);
+    const int64_t shares = attn_shares(a, f.total, 4);
+    if (w >= shares)
         return;
-    const int b = __builtin_amdgcn_readfirstlane(f.seq);
-    const int row0 = __builtin_amdgcn_readfirstlane((int)f.local) * (16 * NT);
+    int64_t u = w * f.total / shares;
+    const int64_t u1 = (w + 1) * f.total / shares;
+    __syncthreads();
+    f = attn_locate(a.seqs, u, false, found, count);
+    int b = __builtin_amdgcn_readfirstlane(f.seq);
+    int64_t at = f.local;  // the unit's number in the sequence
+    while (u < u1) {
+        const AttnSeq s = attn_seq(a, b);
+        const AttnCount c = count(b);
+        if (at >= c.tiles * c.units) {
+            b++;
+            at = 0;
+            continue;
+        }
+        const int tile = __builtin_amdgcn_readfirstlane((int)(at / c.units));
+        const int first = __builtin_amdgcn_readfirstlane((int)(at - tile * c.units));
+        const int units = (int)c.units;
+        const int n = __builtin_amdgcn_readfirstlane(units - first < u1 - u ? units - first : (int)(u1 - u));
+        const int row0 = tile * 16 * NT;
+        int any, none, lo0, hi0, lo1, hi1;  // tokens of the sequence's, the tile's first and last row
+        const int last = (row0 + 16 * NT - 1) / a.group;
+        attn_limits(a, s, 0, &any, &none);
+        attn_limits(a, s, row0 / a.group, &lo0, &hi0);
+        attn_limits(a, s, last < s.nq ? last : s.nq - 1, &lo1, &hi1);
+        AttnWave<D, NT> x;
+        x.open(a, s, h, row0);
+        const int t0 = (any & ~(kAttnStep - 1)) + first * kAttnStep;
+        const int share = (n + tls - 1) / tls * kAttnStep;
+        int from = t0 + tl * share, to = from + share;
+        to = to < t0 + n * kAttnStep ? to : t0 + n * kAttnStep;
+        to = to < hi1 ? to : hi1;
+        from = from > (lo0 & ~(kAttnStep - 1)) ? from : lo0 & ~(kAttnStep - 1);
+        x.walk(a, a.table + b * a.ld_table, h, from, to, lo0, lo1, hi0);
+        x.close();
+        attn_join<D, NT>(x, hl, wave, buf);
+        if (tl == 0) {
+            if (n == units) {
+                attn_finish<D, NT>(a, x, s, h, row0);
+            } else {
+                const int slot = first == 0;
+                float* dst = a.partial + (((int64_t)w * blocks + hb) * 2 + slot) * hl * attn_part<D, NT>() +
+                             (wave % hl) * attn_part<D, NT>() + (threadIdx.x & 63);
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    dst[(t * (D / 4 + 2)) * 64] = x.m[t];
+                    dst[(t * (D / 4 + 2) + 1) * 64] = x.l[t];
+#pragma unroll
+                    for (int i = 0; i < D / 4; i++)
+                        dst[(t * (D / 4 + 2) + 2 + i) * 64] = x.o[t][i >> 2][i & 3];
+                }
+            }
+        }
+        u += n;
+        at += n;
+    }
+}
+
+// Joins what the shares left of one tile of rows (blockIdx.x) for one KV head
+// (blockIdx.y), in the order of the tokens: the weights exp2(m - max) of all
+// parts first, then the weighted sums of o, each wave a run of the parts.
+// blockIdx.z: pieces of 4 output elements per lane.
+constexpr int kAttnParts = 512;  // shares of one tile, at most
+template <int D, int NT>
+__global__ void __launch_bounds__(1024)
+attn_combine_kernel(AttnArgs a)
+{
+    __shared__ int64_t found[kAttnFoundLds];
+    __shared__ float weight[kAttnParts][16];
+    __shared__ float red[16][2][16];
+    __shared__ float4_t sum[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    auto count = [&](int b) { return attn_count<D, NT>(a, b); };
+    const AttnFound f = attn_locate(a.seqs, blockIdx.x, true, found, count);
+    if ((int64_t)blockIdx.x >= f.all_tiles)
+        return;
+    const int b = f.seq;
+    const int64_t units = count(b).units;
+    const int64_t shares = attn_shares(a, f.total, 4);
+    const int64_t u0 = f.before + f.local * units;
+    const int w0 = (int)(((u0 + 1) * shares - 1) / f.total), w1 = (int)(((u0 + units) * shares - 1) / f.total);
+    if (w0 == w1)
+        return;  // one share held the whole tile
+    const int parts = w1 - w0 + 1;
+    const int hl = a.head_lanes, blocks = a.kv_heads / hl;
+    const int h = blockIdx.y, hb = h / hl;
     const AttnSeq s = attn_seq(a, b);
-    int lo0, hi0, lo1, hi1;  // tokens of the first and of the last row
-    const int last = (row0 + 16 * NT - 1) / a.group;
-    attn_limits(a, s, row0 / a.group, &lo0, &hi0);
-    attn_limits(a, s, last < s.nq ? last : s.nq - 1, &lo1, &hi1);
-    AttnWave<D, NT> w;
-    w.open(a, s, h, row0);
-    const int t0 = lo0 & ~(kAttnStep - 1);
-    const int steps = hi1 > t0 ? (hi1 - t0 + kAttnStep - 1) / kAttnStep : 0;
-    const int share = (steps + tls - 1) / tls * kAttnStep;
-    const int from = t0 + tl * share, to = from + share < hi1 ? from + share : hi1;
-    w.walk(a, a.table + b * a.ld_table, h, from, to, lo0, lo1, hi0);
-    attn_join<D, NT>(w, hl, wave, buf);
-    if (tl == 0)
-        attn_finish<D, NT>(a, w, s, h, row0);
+    const int row0 = (int)f.local * 16 * NT;
+    const float vg = *a.v_global;
+    // part p: the share w0 + p, slot 1 of the first, slot 0 of the others
+    auto part = [&](int p) {
+        return a.partial + (((int64_t)(w0 + p) * blocks + hb) * 2 + (p == 0)) * hl * attn_part<D, NT>() +
+               (h - hb * hl) * attn_part<D, NT>();
+    };
+#pragma unroll 1
+    for (int t = 0; t < NT; t++) {
+        const int n = lane & 15;
+        float m = kAttnLow;
+        for (int p = wave * 4 + (lane >> 4); p < parts; p += waves * 4)
+            m = __builtin_fmaxf(m, part(p)[t * (D / 4 + 2) * 64 + n]);
+        m = __builtin_fmaxf(m, __shfl_xor(m, 16, 64));
+        m = __builtin_fmaxf(m, __shfl_xor(m, 32, 64));
+        __syncthreads();
+        if (lane < 16)
+            red[wave][0][n] = m;
+        __syncthreads();
+        for (int i = 0; i < waves; i++)
+            m = __builtin_fmaxf(m, red[i][0][n]);
+        float l = 0.0f;
+        for (int p = wave * 4 + (lane >> 4); p < parts; p += waves * 4) {
+            const float* src = part(p) + t * (D / 4 + 2) * 64 + n;
+            const float g = __builtin_amdgcn_exp2f(src[0] - m);
+            weight[p][n] = g;
+            l += src[64] * g;
+        }
+        l += __shfl_xor(l, 16, 64);
+        l += __shfl_xor(l, 32, 64);
+        if (lane < 16)
+            red[wave][1][n] = l;
+        __syncthreads();
+        l = 0.0f;
+        for (int i = 0; i < waves; i++)
+            l += red[i][1][n];
+        const int r = row0 + 16 * t + n;
+        const int i = r / a.group, head = h * a.group + r - i * a.group;
+        const int64_t token = s.q0 + i;
+        const float scale = l > 0.0f ? vg / l : 0.0f;
+        if (i < s.nq && a.lse && blockIdx.z == 0 && threadIdx.x < 16)
+            a.lse[token * (a.kv_heads * a.group) + head] =
+                l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+        const int run = (parts + waves - 1) / waves, p1 = (wave + 1) * run < parts ? (wave + 1) * run : parts;
+        for (int c = blockIdx.z; c < D / 16; c += gridDim.z) {
+            const int k = c / (D / 64), dd = 4 * (c - k * (D / 64));
+            float4_t o = (float4_t){0, 0, 0, 0};
+#pragma unroll 4
+            for (int p = wave * run; p < p1; p++) {
+                const float* src = part(p) + (t * (D / 4 + 2) + 2 + 4 * dd + k) * 64 + lane;
+                const float g = weight[p][n];
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    o[j] = __builtin_fmaf(src[4 * j * 64], g, o[j]);
+            }
+            __syncthreads();  // the last piece's reads of sum are done
+            sum[wave][lane] = o;
+            __syncthreads();
+            if (wave == 0 && i < s.nq) {
+                for (int q = 1; q < waves; q++)
+                    o += sum[q][lane];
+                *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * (lane >> 4) + k) * (D / 16) + dd) =
+                    (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
+            }
+        }
+        __syncthreads();  // weight and red are written again
+    }
 }
 
 }  // namespace nvfp4

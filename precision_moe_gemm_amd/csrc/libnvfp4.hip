@@ -208,14 +208,47 @@ void launch_kv_append(const AppendArgs& a, hipStream_t st)
     kv_append_kernel<<<dim3((unsigned)gx, gy), 256, 0, st>>>(a);
 }
 
-template <int D>
-nvfp4_status launch_attention(const AttnArgs& a, hipStream_t st)
+// Shares of the row kernel: as many workgroups as the chip holds at once (2
+// per CU) divided over the blocks of KV heads, a multiple of 8.
+int attention_workers(int kv_heads, int head_lanes)
 {
-    const int64_t items = a.n * a.group / 16 + a.seqs;
-    if (items > 0x7FFFFFFF)
+    return std::max(8, 512 / (kv_heads / head_lanes) / 8 * 8);
+}
+
+int attention_head_lanes(int kv_heads) { return kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1); }
+
+size_t attention_ws_bytes(int kv_heads, int64_t D)
+{
+    const int hl = attention_head_lanes(kv_heads);
+    // two slots per share and KV head, 16 rows (32 with two row tiles) of D values, m and l
+    return align256((size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float));
+}
+
+template <int D, int NT>
+nvfp4_status launch_attention_rows(const AttnArgs& a, hipStream_t st)
+{
+    const int64_t tiles = a.n * a.group / (16 * NT) + a.seqs;
+    if (tiles > 0x7FFFFFFF || a.kv_heads > 65535)
         return NVFP4_ERR_UNSUPPORTED;
-    attn_rows_kernel<D, 1><<<dim3((unsigned)items, a.kv_heads / a.head_lanes), kAttnThreads, 0, st>>>(a);
+    const int blocks = a.kv_heads / a.head_lanes;
+    attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), kAttnThreads, 0, st>>>(a);
+    nvfp4_status s = launch_status();
+    if (s != NVFP4_OK)
+        return s;
+    const int64_t z = std::max<int64_t>(1, std::min<int64_t>(D / 16, 512 / (tiles * a.kv_heads)));
+    const unsigned threads = tiles * a.kv_heads * z >= 512 ? 256 : 1024;
+    attn_combine_kernel<D, NT><<<dim3((unsigned)tiles, a.kv_heads, (unsigned)z), threads, 0, st>>>(a);
     return launch_status();
+}
+
+template <int D>
+nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
+{
+    a.head_lanes = attention_head_lanes(a.kv_heads);
+    a.workers = attention_workers(a.kv_heads, a.head_lanes);
+    if (max_q * a.group <= 16)
+        return launch_attention_rows<D, 1>(a, st);
+    return launch_attention_rows<D, 2>(a, st);
 }
 
 // RMS norm: 1024-thread workgroups, up to 8 chunks of 8 elements per thread.
@@ -994,7 +1027,7 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         // T query rows, k query heads, E KV heads, H = head_dim, I = sequences
         if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
             return 0;
-        return 0;
+        return attention_ws_bytes(E, H);
     }
     return 0;
 }
@@ -2158,9 +2191,12 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.out = (uint16_t*)out;
     a.ld_out = ld_out;
     a.lse = lse;
-    a.head_lanes = kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1);
-    nvfp4_status s = D == 64 ? launch_attention<64>(a, S(stream))
-                             : (D == 128 ? launch_attention<128>(a, S(stream)) : launch_attention<256>(a, S(stream)));
+    a.partial = (float*)ws;
+    if (!cu_q)
+        max_q = 1;
+    nvfp4_status s = D == 64    ? launch_attention<64>(a, max_q, S(stream))
+                     : D == 128 ? launch_attention<128>(a, max_q, S(stream))
+                                : launch_attention<256>(a, max_q, S(stream));
     if (s == NVFP4_OK && checks_on()) {
         check_bf16(q, n, q_heads * D, ld_q, S(stream));
         s = check_tensors_data({k_cache, v_cache}, S(stream));
