@@ -24,13 +24,15 @@
 // row for 4 + 4 tokens of two 16-token tiles, which is its share of the
 // second product's B operand as it stands: p never leaves its registers.
 // The order of the contraction elements is free as long as both operands
-// agree on it: the first product gives lane group g = l / 16 the elements
-// [g D / 4, + D / 4), one contiguous piece of a K row; the second gives it
-// tokens 4g .. 4g + 3 of both tiles, and output row m of its MFMA dd is
-// element m D / 16 + dd, so a lane reads a contiguous piece of a V row too.
-// Neither operand passes through shared memory.
+// agree on it, and so is the order of a tile's rows: with n = l % 16 and
+// g = l / 16, the first product gives lane group g the elements [g D / 4,
+// + D / 4), one contiguous piece of a K row, and row n is token
+// 4 (n % 4) + n / 4; so output row 4g + i is token 4i + g, and the second
+// product gives group g tokens 4i + g of both tiles; its output row m of MFMA
+// dd is element m D / 16 + dd, so a lane needs a contiguous piece of a V row.
 #pragma once
 #include "common.h"
+#include "gemm.h"
 
 namespace nvfp4 {
 
@@ -58,10 +60,12 @@ struct AttnArgs {
     float* lse;              // [n, heads] or null
     int head_lanes;          // KV heads a workgroup holds side by side (1, 2 or 4)
     int workers;             // shares that the tokens are cut into (at most)
-    float* partial;          // what shares leave of sequences that they hold a part of
+    struct AttnTile* tiles;  // tiles of rows, as the joining launch needs them
+    float* partial;          // what shares leave of tiles that they hold a part of
 };
 
 constexpr int kAttnThreads = 256;
+typedef __attribute__((address_space(3))) void* attn_lds_t;
 constexpr int kAttnStep = 32;            // tokens of one step
 constexpr float kAttnLow = -1e30f;       // running maximum of a row that has seen nothing
 constexpr float kAttnLazy = 8.0f;        // growth of the maximum (log 2) that is let pass
@@ -72,6 +76,10 @@ constexpr float kAttnLift = 7.0f;        // p is held times 2^7, at most 2^15 (f
 struct AttnSeq {
     int q0, nq, kv;
 };
+
+// The value of a variable that is the same in all lanes, held in a scalar
+// register: addresses and branches that depend on it are then scalar too.
+NVFP4_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 NVFP4_DEV AttnSeq attn_seq(const AttnArgs& a, int b)
 {
@@ -110,79 +118,84 @@ NVFP4_DEV void attn_limits(const AttnArgs& a, const AttnSeq& s, int i, int* star
     *start = b < 0 ? 0 : b;
 }
 
-// Work of a row kernel is counted in units: sequence b has tiles(b) tiles of
-// rows and units(b) steps of tokens for each of them (at least one, so that
-// rows that see nothing are written too).  The sequence that holds unit x (or
-// tile x, by_tile), the number of that unit (tile) in the sequence, the units
-// before the sequence and the units of all sequences.  All threads of the
-// workgroup call it; every thread sums a contiguous run of sequences.
+NVFP4_DEV AttnSeq attn_seq_uniform(const AttnArgs& a, int b)
+{
+    const AttnSeq s = attn_seq(a, b);
+    return AttnSeq{uniform(s.q0), uniform(s.nq), uniform(s.kv)};
+}
+
+// Work of a row kernel is counted in units: sequence b has `tiles` tiles of
+// rows and `units` steps of tokens for each of them (at least one, so that
+// rows that see nothing are written too).  The host refuses launches whose
+// units could pass 31 bits.
 struct AttnCount {
-    int64_t tiles, units;
-};
-struct AttnFound {
-    int64_t local, before, total, all_tiles;
-    int seq;
+    int tiles, units;
 };
 
-constexpr int kAttnFoundLds = 2 * 16 + 3;
+// Every wave scans all sequences by itself: lane l sums the run of
+// sequences [l per, + per).
+struct AttnScan {
+    AttnCount before;  // tiles and units before this lane's run
+    int mine;          // units of the run
+    int tiles, units;  // of all sequences
+};
 
 template <class Count>
-NVFP4_DEV AttnFound attn_locate(int seqs, int64_t x, bool by_tile, int64_t* lds, Count count)
+NVFP4_DEV AttnScan attn_scan(int seqs, Count count)
 {
-    const int nt = blockDim.x, waves = nt >> 6, wave = threadIdx.x >> 6;
-    const int per = (seqs + nt - 1) / nt;
-    const int b0 = threadIdx.x * per, b1 = b0 + per < seqs ? b0 + per : seqs;
-    AttnCount mine = {0, 0};
+    const int lane = threadIdx.x & 63;
+    const int per = (seqs + 63) >> 6;
+    const int b0 = lane * per, b1 = b0 + per < seqs ? b0 + per : seqs;
+    int tiles = 0, units = 0;
     for (int b = b0; b < b1; b++) {
         const AttnCount c = count(b);
-        mine.tiles += c.tiles;
-        mine.units += c.tiles * c.units;
+        tiles += c.tiles;
+        units += c.tiles * c.units;
     }
-    AttnCount up = mine;  // inclusive sums over the wave's lanes
+    int ut = tiles, uu = units;  // inclusive sums over the lanes
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int64_t a = __shfl_up(up.tiles, off, 64), u = __shfl_up(up.units, off, 64);
-        const bool in = (int)(threadIdx.x & 63) >= off;
-        up.tiles += in ? a : 0;
-        up.units += in ? u : 0;
+        const int x = __shfl_up(ut, off, 64), y = __shfl_up(uu, off, 64);
+        ut += lane >= off ? x : 0;
+        uu += lane >= off ? y : 0;
     }
-    if ((threadIdx.x & 63) == 63) {
-        lds[2 * wave] = up.tiles;
-        lds[2 * wave + 1] = up.units;
-    }
-    __syncthreads();
-    AttnCount before = {0, 0}, total = {0, 0};
-    for (int w = 0; w < waves; w++) {
-        before.tiles += w < wave ? lds[2 * w] : 0;
-        before.units += w < wave ? lds[2 * w + 1] : 0;
-        total.tiles += lds[2 * w];
-        total.units += lds[2 * w + 1];
-    }
-    before.tiles += up.tiles - mine.tiles;
-    before.units += up.units - mine.units;
-    int64_t rest = x - (by_tile ? before.tiles : before.units);
-    if (rest >= 0 && rest < (by_tile ? mine.tiles : mine.units)) {
-        int b = b0;
-        for (; b < b1; b++) {
-            const AttnCount c = count(b);
-            const int64_t size = by_tile ? c.tiles : c.tiles * c.units;
-            if (rest < size)
-                break;
-            rest -= size;
-            before.units += c.tiles * c.units;
-        }
-        lds[32] = rest;
-        lds[33] = before.units;
-        lds[34] = b;
-    }
-    __syncthreads();
+    AttnScan s;
+    s.before.tiles = ut - tiles;
+    s.before.units = uu - units;
+    s.mine = units;
+    s.tiles = __builtin_amdgcn_readlane(ut, 63);
+    s.units = __builtin_amdgcn_readlane(uu, 63);
+    return s;
+}
+
+// The sequence that holds unit u (u < s.units), the unit's number in it and
+// the tiles and units before it: all uniform.
+struct AttnFound {
+    int seq, at;
+    AttnCount before;
+};
+
+template <class Count>
+NVFP4_DEV AttnFound attn_find(const AttnScan& s, int seqs, int u, Count count)
+{
+    const int per = (seqs + 63) >> 6;
+    const uint64_t hit = __ballot(u >= s.before.units && u - s.before.units < s.mine);
+    const int l = __builtin_ctzll(hit);
     AttnFound f;
-    f.local = lds[32];
-    f.before = lds[33];
-    f.total = total.units;
-    f.all_tiles = total.tiles;
-    f.seq = (int)lds[34];
-    return f;
+    f.seq = l * per;
+    f.before.tiles = __builtin_amdgcn_readlane(s.before.tiles, l);
+    f.before.units = __builtin_amdgcn_readlane(s.before.units, l);
+    f.at = u - f.before.units;
+    for (;;) {
+        const AttnCount c = count(f.seq);
+        const int tiles = uniform(c.tiles), units = uniform(c.tiles * c.units);
+        if (f.at < units)
+            return f;
+        f.at -= units;
+        f.before.tiles += tiles;
+        f.before.units += units;
+        f.seq++;
+    }
 }
 
 NVFP4_DEV float4_t mfma16(half8_t a, half8_t b, float4_t c)
@@ -208,30 +221,52 @@ NVFP4_DEV half8_t decode_row8(uint32_t w, half2_t s)
     return (half8_t){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+// Wait until at most N copies are in flight, with the reads of the older ones
+// to follow.  The compiler would have such a read wait for every copy (it
+// takes them for flat accesses, which may finish out of order) if it had not
+// seen this wait take effect, which an instruction behind it ensures.
+template <int N>
+NVFP4_DEV void wait_copies()
+{
+    wait_vm<N>();
+    asm volatile("s_nop 0" ::: "memory");
+}
+
 // A wave's lanes: query column n, lane group g.
 NVFP4_DEV int lane_n() { return threadIdx.x & 15; }
 NVFP4_DEV int lane_g() { return (threadIdx.x >> 4) & 3; }
 
-// What a lane holds of one step's 32 tokens of K and V, as read.
+// A wave's copy of 32 tokens of K or V in shared memory: codes [32][D / 2],
+// then scales [32][D / 16].  It is filled by direct copies of 16 bytes per
+// lane (4 for scales below 16 bytes a row) in which neighbouring lanes take
+// neighbouring bytes of a row: read straight into registers, the operands
+// need 20 loads of 1 to 16 bytes per lane whose neighbours lie in different
+// rows, and ran at 3.3 TB/s where the wide copies of the same bytes reach 5.0
+// (32 query heads, 8 KV heads of 128).  Chunk c (16 bytes) of row r lies in
+// slot c ^ attn_swz(r) of the row, which spreads the 16 rows of a K read over
+// the banks.
 template <int D>
-struct AttnRaw {
-    uint32_t kc[2][D / 32];                  // K codes: token n of each 16, elements [g D / 4, + D / 4)
-    uint32_t ks[2];                          // their scale bytes (D / 64)
-    uint32_t vc[8][D > 128 ? D / 128 : 1];   // V codes: tokens 4g + j of each 16, elements [n D / 16, + D / 16)
-    uint32_t vs[8];                          // their scale byte
-};
+constexpr int attn_stage() { return 16 * D + (D == 256 ? 1024 : 256); }
+
+template <int D>
+NVFP4_DEV int attn_swz(int r)
+{
+    return D == 64 ? 0 : (D == 128 ? (r >> 2) & 3 : (r >> 1) & 7);
+}
 
 // The pages of a wave's token range: lane l holds the entry of page
-// first + l of the sequence (-1: not a page of the cache).
+// first + l of the sequence (-1: not a page of the cache).  (idx, off): the
+// page and the place in it of the next 16 tokens to be read.
 struct AttnPages {
     const int32_t* row;
     int first, last;
     int needed;  // first page with a token that some row sees (a page before it may be gone)
+    int idx, off;
     int entry;
-    NVFP4_DEV void fill(const AttnArgs& a, int idx)
+    NVFP4_DEV void fill(const AttnArgs& a, int i0)
     {
-        first = idx;
-        int i = idx + (int)(threadIdx.x & 63);
+        first = i0;
+        int i = i0 + (int)(threadIdx.x & 63);
         i = i < last ? i : last;
         const int e = row[i];
         const bool ok = e >= 0 && e < a.num_pages;
@@ -239,11 +274,19 @@ struct AttnPages {
             raise_error(NVFP4_ERR_RANGE);
         entry = ok ? e : -1;
     }
-    NVFP4_DEV int get(const AttnArgs& a, int idx)
+    NVFP4_DEV int get(const AttnArgs& a)
     {
-        if (idx - first >= 64)
-            fill(a, idx);
-        return __builtin_amdgcn_readlane(entry, idx - first);
+        const int i = idx < last ? idx : last;  // past the end: any page, masked
+        if (i - first >= 64)
+            fill(a, i);
+        return __builtin_amdgcn_readlane(entry, i - first);
+    }
+    NVFP4_DEV void next(const AttnArgs& a)
+    {
+        off += 16;
+        const bool over = off == a.page;
+        off = over ? 0 : off;
+        idx += over;
     }
 };
 
@@ -254,11 +297,19 @@ struct AttnWave {
     float4_t o[NT][D / 16];
     float m[NT], l[NT], c1[NT];
     int start[NT], end[NT];
+    // the lane's part of the copies: its place in 16 tokens' codes (of the even and the odd copies of a
+    // half) and its row among the 32 tokens' scales
+    uint32_t co[2], so;
 
     // rows row0 .. row0 + 16 NT of sequence s: row r is query token r / group, head r % group of KV head h
     NVFP4_DEV void open(const AttnArgs& a, const AttnSeq& s, int h, int row0)
     {
         const float kg = *a.k_global;
+        const uint32_t lane = threadIdx.x & 63, stride = a.kv_heads;
+        const uint32_t r = (lane / (D / 32)) & 15, c = lane % (D / 32);
+        co[0] = r * stride * (D / 2) + 16 * (c ^ attn_swz<D>(r));
+        co[1] = D == 256 ? (r + 8) * stride * (D / 2) + 16 * (c ^ attn_swz<D>(r + 8)) : co[0];
+        so = D == 128 ? ((lane >> 1) & 15) * stride * (D / 16) + 4 * (lane & 1) : (lane & 15) * stride * (D / 16);
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const int r = row0 + 16 * t + lane_n();
@@ -300,55 +351,64 @@ struct AttnWave {
         }
     }
 
-    // the 16 tokens of half `half` of a step: they lie in one page.  The first
-    // token's row is the same for all lanes, so it goes into the scalar base
-    // of the loads and the lane's part is 32 bits.
-    NVFP4_DEV void load_half(const AttnArgs& a, AttnRaw<D>& raw, int half, int h, int64_t tok) const
+    // Copies of one step of K (or V).
+    static constexpr int kCopies = D == 64 ? 2 : (D == 128 ? 3 : 5);
+
+    // request the 32 tokens of K (or V) whose halves begin at cache rows row[]
+    NVFP4_DEV void request(const uint8_t* packed, const uint8_t* scales, const int64_t (&row)[2], uint8_t* dst) const
     {
-        const int64_t row = tok * a.kv_heads + h;  // the first token's cache row
-        const uint32_t stride = a.kv_heads;
-        const uint8_t* kc = a.k_packed + row * (D / 2) + (uint32_t)(lane_n() * stride * (D / 2) + lane_g() * (D / 8));
-        const uint8_t* ks = a.k_scales + row * (D / 16) + (uint32_t)(lane_n() * stride * (D / 16) + lane_g() * (D / 64));
+        const int lane = threadIdx.x & 63;
+        wait_lgkm0();  // the reads of dst's last step are done
+        const int64_t apart = row[1] - row[0];
         if constexpr (D == 64) {
-            const u32x2 w = *(const u32x2*)kc;
-            raw.kc[half][0] = w.x;
-            raw.kc[half][1] = w.y;
-            raw.ks[half] = *ks;
+            __builtin_amdgcn_global_load_lds((const void*)(packed + (row[0] + (lane < 32 ? 0 : apart)) * (D / 2) + co[0]),
+                                             (attn_lds_t)dst, 16, 0, 0);
         } else {
 #pragma unroll
-            for (int c = 0; c < D / 128; c++) {
-                const u32x4 w = ((const u32x4*)kc)[c];
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    raw.kc[half][4 * c + i] = w[i];
-            }
-            if constexpr (D == 128)
-                raw.ks[half] = *(const uint16_t*)ks;
-            else
-                raw.ks[half] = *(const uint32_t*)ks;
+            for (int i = 0; i < D / 64; i++)
+                __builtin_amdgcn_global_load_lds(
+                    (const void*)(packed + row[i / (D / 128)] * (D / 2) + co[D == 256 ? i & 1 : 0]),
+                    (attn_lds_t)(dst + i * 1024), 16, 0, 0);
         }
-        const uint32_t vo = 4 * lane_g() * stride * (D / 2) + lane_n() * (D / 32);
-        const uint32_t so = 4 * lane_g() * stride * (D / 16) + lane_n() * D / 256;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint8_t* p = a.v_packed + (row + j * (int64_t)stride) * (D / 2) + vo;
-            if constexpr (D == 64) {
-                raw.vc[4 * half + j][0] = *(const uint16_t*)p;
-            } else if constexpr (D == 128) {
-                raw.vc[4 * half + j][0] = *(const uint32_t*)p;
-            } else {
-                const u32x2 w = *(const u32x2*)p;
-                raw.vc[4 * half + j][0] = w.x;
-                raw.vc[4 * half + j][1] = w.y;
-            }
-            raw.vs[4 * half + j] = a.v_scales[(row + j * (int64_t)stride) * (D / 16) + so];
-        }
+        // D = 128: two lanes per row; else one (lanes 32 .. 63 copy the same again, behind)
+        const bool second = D == 128 ? lane >= 32 : (lane & 16) != 0;
+        const uint8_t* src = scales + (row[0] + (second ? apart : 0)) * (D / 16) + so;
+        if constexpr (D == 256)
+            __builtin_amdgcn_global_load_lds((const void*)src, (attn_lds_t)(dst + 16 * D), 16, 0, 0);
+        else
+            __builtin_amdgcn_global_load_lds((const void*)src, (attn_lds_t)(dst + 16 * D), 4, 0, 0);
     }
 
-    // one step: tokens t0 .. t0 + 32; ok: which halves lie in a page of the cache
-    NVFP4_DEV void step(const AttnRaw<D>& raw, int t0, bool inside, const bool (&ok)[2])
+    // S^T of one step: tokens t0 .. t0 + 32 from a finished copy of K
+    NVFP4_DEV void scores(const uint8_t* src, float4_t (&s)[NT][2]) const
     {
-        float4_t s[NT][2];
+        const int n = lane_n(), g = lane_g();
+        const int kt = 4 * (n & 3) + (n >> 2);  // row n of a K tile
+        uint32_t kc[2][D / 32], ks[2];
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            const int k = (16 * half + kt) * (D / 2);
+            if constexpr (D == 64) {
+                const u32x2 w = *(const u32x2*)(src + (k + 8 * g));
+                kc[half][0] = w.x;
+                kc[half][1] = w.y;
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 128; c++) {
+                    const u32x4 w = *(const u32x4*)(src + (k + 16 * ((g * (D / 128) + c) ^ attn_swz<D>(kt))));
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        kc[half][4 * c + i] = w[i];
+                }
+            }
+            const int b = 16 * D + (16 * half + kt) * (D / 16) + g * (D / 64);
+            if constexpr (D == 64)
+                ks[half] = src[b];
+            else if constexpr (D == 128)
+                ks[half] = *(const uint16_t*)(src + b);
+            else
+                ks[half] = *(const uint32_t*)(src + b);
+        }
 #pragma unroll
         for (int half = 0; half < 2; half++) {
 #pragma unroll
@@ -356,14 +416,18 @@ struct AttnWave {
                 s[t][half] = (float4_t){0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < D / 32; c++) {
-                const uint32_t b = raw.ks[half] >> (8 * (c >> 1));
-                const half8_t k = decode_row8(raw.kc[half][c], scale_pair(b, b));
+                const uint32_t b = ks[half] >> (8 * (c >> 1));
+                const half8_t k = decode_row8(kc[half][c], scale_pair(b, b));
 #pragma unroll
                 for (int t = 0; t < NT; t++)
                     s[t][half] = mfma16(k, q[t][c], s[t][half]);
             }
         }
-        half8_t p[NT];
+    }
+
+    // P^T of one step; ok: which halves lie in a page of the cache
+    NVFP4_DEV void weights(float4_t (&s)[NT][2], half8_t (&p)[NT], int t0, bool inside, const bool (&ok)[2])
+    {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             if (!inside) {
@@ -371,7 +435,7 @@ struct AttnWave {
                 for (int half = 0; half < 2; half++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const int tok = t0 + 16 * half + 4 * lane_g() + i;
+                        const int tok = t0 + 16 * half + 4 * i + lane_g();
                         const bool seen = ok[half] && tok >= start[t] && tok < end[t];
                         s[t][half][i] = seen ? s[t][half][i] : -__builtin_inff();
                     }
@@ -402,17 +466,41 @@ struct AttnWave {
             for (int i = 0; i < 8; i++)
                 p[t][i] = (_Float16)e[i];
         }
+    }
+
+    // O^T += V^T P^T of one step from a finished copy of V
+    NVFP4_DEV void values(const uint8_t* src, const half8_t (&p)[NT])
+    {
+        const int n = lane_n(), g = lane_g();
+        uint32_t vc[8][D > 128 ? D / 128 : 1], vs[8];
+#pragma unroll
+        for (int half = 0; half < 2; half++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int r = 4 * j + g;
+                const int v = (16 * half + r) * (D / 2);
+                if constexpr (D == 64) {
+                    vc[4 * half + j][0] = *(const uint16_t*)(src + (v + 2 * n));
+                } else if constexpr (D == 128) {
+                    vc[4 * half + j][0] = *(const uint32_t*)(src + (v + 16 * ((n >> 2) ^ attn_swz<D>(r)) + 4 * (n & 3)));
+                } else {
+                    const u32x2 w = *(const u32x2*)(src + (v + 16 * ((n >> 1) ^ attn_swz<D>(r)) + 8 * (n & 1)));
+                    vc[4 * half + j][0] = w.x;
+                    vc[4 * half + j][1] = w.y;
+                }
+                vs[4 * half + j] = src[16 * D + (16 * half + r) * (D / 16) + n * D / 256];
+            }
         half2_t sc[4];
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            sc[j] = scale_pair(raw.vs[2 * j], raw.vs[2 * j + 1]);
+            sc[j] = scale_pair(vs[2 * j], vs[2 * j + 1]);
         // token pairs side by side: byte i of even / odd holds elements 2i / 2i + 1 of both tokens
 #pragma unroll
         for (int w = 0; w < (D > 128 ? D / 128 : 1); w++) {
             uint32_t even[4], odd[4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const uint32_t x = raw.vc[2 * j][w], y = raw.vc[2 * j + 1][w];
+                const uint32_t x = vc[2 * j][w], y = vc[2 * j + 1][w];
                 even[j] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
                 odd[j] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
             }
@@ -442,26 +530,25 @@ struct AttnWave {
         }
     }
 
-    // the step at token t0 + 32 k of a walk (the last one again past the end)
-    NVFP4_DEV void load(const AttnArgs& a, AttnPages& pages, AttnRaw<D>& raw, bool (&ok)[2], int h, int t) const
+    // the cache rows of the next 32 tokens' halves; ok: which lie in a page of the cache
+    NVFP4_DEV void rows(const AttnArgs& a, AttnPages& pages, int64_t (&row)[2], bool (&ok)[2], int h) const
     {
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-            int i = (t + 16 * half) / a.page;
-            const int off = t + 16 * half - i * a.page;
-            i = i < pages.last ? i : pages.last;  // past the end: any page, masked
-            const int page = pages.get(a, i);
+            const int page = pages.get(a);
             ok[half] = page >= 0;
-            load_half(a, raw, half, h, (int64_t)(page < 0 ? 0 : page) * a.page + off);
+            row[half] = ((int64_t)(page < 0 ? 0 : page) * a.page + pages.off) * a.kv_heads + h;
+            pages.next(a);
         }
     }
 
     // tokens [t0, t1) (t0 a multiple of 32); any: the first token that some
-    // row sees; [lo, hi): the tokens that every row sees.  Each step's data is
-    // requested while the step before it is computed; the requests are
-    // unconditional (past the end the last step's, which is in the cache), so
-    // that the compiler can count them and wait for the older step only.
-    NVFP4_DEV void walk(const AttnArgs& a, const int32_t* table_row, int h, int t0, int t1, int any, int lo, int hi)
+    // row sees; [lo, hi): the tokens that every row sees.  The next step's K is
+    // requested as soon as this step's is in registers, and V likewise, so
+    // that one of them is always under way.  Past the end the requests go to
+    // the last page again (lines that are near) and the copy is not used.
+    NVFP4_DEV void walk(const AttnArgs& a, const int32_t* table_row, int h, int t0, int t1, int any, int lo, int hi,
+                        uint8_t* bufk, uint8_t* bufv)
     {
         if (t0 >= t1)
             return;
@@ -469,19 +556,29 @@ struct AttnWave {
         pages.row = table_row;
         pages.last = (t1 - 1) / a.page;
         pages.needed = any / a.page;
-        pages.fill(a, t0 / a.page);
-        const int end = t0 + (t1 - t0 - 1) / kAttnStep * kAttnStep;  // the last step
-        AttnRaw<D> x, y;
-        bool okx[2], oky[2];
-        load(a, pages, x, okx, h, t0);
-        for (int t = t0; t <= end; t += 2 * kAttnStep) {
-            const int u = t + kAttnStep, v = u + kAttnStep;
-            load(a, pages, y, oky, h, u < end ? u : end);
-            step(x, t, okx[0] && okx[1] && t >= lo && u <= hi, okx);
-            load(a, pages, x, okx, h, v < end ? v : end);
-            if (u <= end)
-                step(y, u, oky[0] && oky[1] && u >= lo && v <= hi, oky);
+        pages.idx = t0 / a.page;
+        pages.off = t0 - pages.idx * a.page;
+        pages.fill(a, pages.idx);
+        int64_t row[2];
+        bool ok[2], next[2];
+        rows(a, pages, row, ok, h);
+        request(a.k_packed, a.k_scales, row, bufk);
+        request(a.v_packed, a.v_scales, row, bufv);
+        for (int t = t0; t < t1; t += kAttnStep) {
+            float4_t s[NT][2];
+            half8_t p[NT];
+            wait_copies<kCopies>();
+            scores(bufk, s);
+            rows(a, pages, row, next, h);
+            request(a.k_packed, a.k_scales, row, bufk);
+            weights(s, p, t, ok[0] && ok[1] && t >= lo && t + kAttnStep <= hi, ok);
+            wait_copies<kCopies>();
+            values(bufv, p);
+            request(a.v_packed, a.v_scales, row, bufv);
+            ok[0] = next[0];
+            ok[1] = next[1];
         }
+        wait_vm<0>();
     }
 
     // the sums of the lane groups
@@ -568,27 +665,38 @@ NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT>& w, const At
 template <int D, int NT>
 constexpr int attn_part() { return (D / 4 + 2) * NT * 64; }
 
-// The shares: the units of all sequences in a row, cut into equal runs, at
-// least `least` units each.  Share w holds units [w T / W, (w + 1) T / W).
-NVFP4_DEV int64_t attn_shares(const AttnArgs& a, int64_t total, int least)
+// Rows of 16 that a part keeps: value e of row n and lane group g is at
+// (4 e + g) rows + n (0: m, 1: l, 2 + i: o).
+NVFP4_DEV int attn_part_rows(int left) { return left < 0 ? 0 : (left < 16 ? left : 16); }
+
+// The shares: the units of all sequences in a row, cut into equal runs of at
+// least kAttnLeast units.  Share w holds units [w T / W, (w + 1) T / W).
+constexpr int kAttnLeast = 4;
+NVFP4_DEV int attn_shares(const AttnArgs& a, int total)
 {
-    const int64_t most = (total + least - 1) / least;
+    const int most = (total + kAttnLeast - 1) / kAttnLeast;
     return most < a.workers ? most : a.workers;
 }
 
 template <int D, int NT>
-NVFP4_DEV AttnCount attn_count(const AttnArgs& a, int b)
+NVFP4_DEV AttnCount attn_count(const AttnArgs& a, const AttnSeq& s)
 {
-    const AttnSeq s = attn_seq(a, b);
     int lo0, hi0, lo1, hi1;
     attn_limits(a, s, 0, &lo0, &hi0);
     attn_limits(a, s, s.nq > 0 ? s.nq - 1 : 0, &lo1, &hi1);
     const int t0 = lo0 & ~(kAttnStep - 1);
     AttnCount c;
-    c.tiles = ((int64_t)s.nq * a.group + 16 * NT - 1) / (16 * NT);
+    c.tiles = (s.nq * a.group + 16 * NT - 1) / (16 * NT);
     c.units = hi1 > t0 ? (hi1 - t0 + kAttnStep - 1) / kAttnStep : 1;
     return c;
 }
+
+// A tile of rows as the row kernel leaves it to the joining one: the first of
+// the `parts` shares that hold its tokens, and its rows.  Entry 0 of the list
+// holds the number of tiles in `parts`, entry 1 + i tile i.
+struct AttnTile {
+    int first, parts, q0, nq, row0, pad[3];
+};
 
 // Few query rows per sequence (decode, drafts): the time is the K and V
 // bytes' way from HBM.  The tokens of all sequences are cut into equal shares,
@@ -602,40 +710,44 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1)))
 attn_rows_kernel(AttnArgs a)
 {
-    __shared__ int64_t found[kAttnFoundLds];
-    __shared__ float buf[2 * attn_part<D, NT>()];
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    // the waves' copies of K and V; between walks the space of joined waves
+    constexpr int kStages = 4 * attn_stage<D>(), kJoin = 2 * attn_part<D, NT>() * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t bufk[kStages > kJoin ? kStages : kJoin];
+    __shared__ __attribute__((aligned(16))) uint8_t bufv[kStages];
+    const int wave = uniform((int)(threadIdx.x >> 6));
     const int hl = a.head_lanes, tls = (kAttnThreads / 64) / hl;
     // workgroups go to the 8 XCDs in turn: the head blocks of one share go to
     // the same one, whose L2 then holds the lines that they share
     const int blocks = a.kv_heads / hl;
     const int hb = blockIdx.x / 8 % blocks, w = blockIdx.x / (8 * blocks) * 8 + blockIdx.x % 8;
     const int h = hb * hl + wave % hl, tl = wave / hl;
-    auto count = [&](int b) { return attn_count<D, NT>(a, b); };
-    // (the total first: the share's bounds need it)
-    AttnFound f = attn_locate(a.seqs, 0, false, found, count);
-    const int64_t shares = attn_shares(a, f.total, 4);
+    auto count = [&](int b) { return attn_count<D, NT>(a, attn_seq(a, b)); };
+    const AttnScan scan = attn_scan(a.seqs, count);
+    const int64_t total = scan.units, shares = attn_shares(a, scan.units);
+    if (w == 0 && hb == 0 && threadIdx.x == 0)
+        a.tiles[0].parts = scan.tiles;
     if (w >= shares)
         return;
-    int64_t u = w * f.total / shares;
-    const int64_t u1 = (w + 1) * f.total / shares;
-    __syncthreads();
-    f = attn_locate(a.seqs, u, false, found, count);
-    int b = __builtin_amdgcn_readfirstlane(f.seq);
-    int64_t at = f.local;  // the unit's number in the sequence
+    int u = (int)(w * total / shares);
+    const int u1 = (int)((w + 1) * total / shares);
+    AttnFound f = attn_find(scan, a.seqs, u, count);
     while (u < u1) {
-        const AttnSeq s = attn_seq(a, b);
-        const AttnCount c = count(b);
-        if (at >= c.tiles * c.units) {
-            b++;
-            at = 0;
+        const AttnSeq s = attn_seq_uniform(a, f.seq);
+        const AttnCount c = attn_count<D, NT>(a, s);
+        if (f.at >= c.tiles * c.units) {
+            f.before.tiles += c.tiles;
+            f.before.units += c.tiles * c.units;
+            f.seq++;
+            f.at = 0;
             continue;
         }
-        const int tile = __builtin_amdgcn_readfirstlane((int)(at / c.units));
-        const int first = __builtin_amdgcn_readfirstlane((int)(at - tile * c.units));
-        const int units = (int)c.units;
-        const int n = __builtin_amdgcn_readfirstlane(units - first < u1 - u ? units - first : (int)(u1 - u));
+        const int tile = f.at / c.units, first = f.at - tile * c.units;
+        const int n = c.units - first < u1 - u ? c.units - first : u1 - u;
         const int row0 = tile * 16 * NT;
+        if (first == 0 && hb == 0 && threadIdx.x == 0) {
+            const int64_t end = u + c.units;  // the share of the tile's last unit
+            a.tiles[1 + f.before.tiles + tile] = AttnTile{w, (int)((end * shares - 1) / total) - w + 1, s.q0, s.nq, row0};
+        }
         int any, none, lo0, hi0, lo1, hi1;  // tokens of the sequence's, the tile's first and last row
         const int last = (row0 + 16 * NT - 1) / a.group;
         attn_limits(a, s, 0, &any, &none);
@@ -649,61 +761,60 @@ attn_rows_kernel(AttnArgs a)
         to = to < t0 + n * kAttnStep ? to : t0 + n * kAttnStep;
         to = to < hi1 ? to : hi1;
         from = from > (lo0 & ~(kAttnStep - 1)) ? from : lo0 & ~(kAttnStep - 1);
-        x.walk(a, a.table + b * a.ld_table, h, from, to, lo0, lo1, hi0);
+        x.walk(a, a.table + f.seq * a.ld_table, h, from, to, lo0, lo1, hi0,
+               bufk + wave * attn_stage<D>(), bufv + wave * attn_stage<D>());
         x.close();
-        attn_join<D, NT>(x, hl, wave, buf);
+        if (tls > 1) {
+            attn_join<D, NT>(x, hl, wave, (float*)bufk);
+            __syncthreads();
+        }
         if (tl == 0) {
-            if (n == units) {
+            if (n == c.units) {
                 attn_finish<D, NT>(a, x, s, h, row0);
             } else {
                 const int slot = first == 0;
                 float* dst = a.partial + (((int64_t)w * blocks + hb) * 2 + slot) * hl * attn_part<D, NT>() +
-                             (wave % hl) * attn_part<D, NT>() + (threadIdx.x & 63);
+                             (wave % hl) * attn_part<D, NT>();
 #pragma unroll
                 for (int t = 0; t < NT; t++) {
-                    dst[(t * (D / 4 + 2)) * 64] = x.m[t];
-                    dst[(t * (D / 4 + 2) + 1) * 64] = x.l[t];
+                    const int rows = attn_part_rows(s.nq * a.group - row0 - 16 * t);
+                    float* p = dst + t * (D / 4 + 2) * 64 + lane_g() * rows + lane_n();
+                    if (lane_n() < rows) {
+                        p[0] = x.m[t];
+                        p[4 * rows] = x.l[t];
 #pragma unroll
-                    for (int i = 0; i < D / 4; i++)
-                        dst[(t * (D / 4 + 2) + 2 + i) * 64] = x.o[t][i >> 2][i & 3];
+                        for (int i = 0; i < D / 4; i++)
+                            p[(2 + i) * 4 * rows] = x.o[t][i >> 2][i & 3];
+                    }
                 }
             }
         }
         u += n;
-        at += n;
+        f.at += n;
     }
 }
 
 // Joins what the shares left of one tile of rows (blockIdx.x) for one KV head
-// (blockIdx.y), in the order of the tokens: the weights exp2(m - max) of all
-// parts first, then the weighted sums of o, each wave a run of the parts.
-// blockIdx.z: pieces of 4 output elements per lane.
-constexpr int kAttnParts = 512;  // shares of one tile, at most
+// (blockIdx.y), in the order of the tokens: max and sum over all parts first,
+// then the sums of o with the weights exp2(m - max).  A piece of 4 output
+// elements per lane at a time: `pieces` waves take different pieces, the
+// others (few tiles with many parts each) different runs of the parts.
 template <int D, int NT>
 __global__ void __launch_bounds__(1024)
-attn_combine_kernel(AttnArgs a)
+attn_combine_kernel(AttnArgs a, int pieces)
 {
-    __shared__ int64_t found[kAttnFoundLds];
-    __shared__ float weight[kAttnParts][16];
     __shared__ float red[16][2][16];
     __shared__ float4_t sum[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    auto count = [&](int b) { return attn_count<D, NT>(a, b); };
-    const AttnFound f = attn_locate(a.seqs, blockIdx.x, true, found, count);
-    if ((int64_t)blockIdx.x >= f.all_tiles)
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int wave = uniform((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
+    if ((int)blockIdx.x >= a.tiles[0].parts)
         return;
-    const int b = f.seq;
-    const int64_t units = count(b).units;
-    const int64_t shares = attn_shares(a, f.total, 4);
-    const int64_t u0 = f.before + f.local * units;
-    const int w0 = (int)(((u0 + 1) * shares - 1) / f.total), w1 = (int)(((u0 + units) * shares - 1) / f.total);
-    if (w0 == w1)
+    const AttnTile tile = a.tiles[1 + blockIdx.x];
+    const int parts = uniform(tile.parts), w0 = uniform(tile.first);
+    if (parts == 1)
         return;  // one share held the whole tile
-    const int parts = w1 - w0 + 1;
     const int hl = a.head_lanes, blocks = a.kv_heads / hl;
     const int h = blockIdx.y, hb = h / hl;
-    const AttnSeq s = attn_seq(a, b);
-    const int row0 = (int)f.local * 16 * NT;
     const float vg = *a.v_global;
     // part p: the share w0 + p, slot 1 of the first, slot 0 of the others
     auto part = [&](int p) {
@@ -712,63 +823,72 @@ attn_combine_kernel(AttnArgs a)
     };
 #pragma unroll 1
     for (int t = 0; t < NT; t++) {
-        const int n = lane & 15;
-        float m = kAttnLow;
-        for (int p = wave * 4 + (lane >> 4); p < parts; p += waves * 4)
-            m = __builtin_fmaxf(m, part(p)[t * (D / 4 + 2) * 64 + n]);
-        m = __builtin_fmaxf(m, __shfl_xor(m, 16, 64));
-        m = __builtin_fmaxf(m, __shfl_xor(m, 32, 64));
-        __syncthreads();
-        if (lane < 16)
+        const int left = tile.nq * a.group - tile.row0 - 16 * t, rows = attn_part_rows(left);
+        if (rows == 0)
+            break;
+        const bool in = n < rows;
+        const int base = t * (D / 4 + 2) * 64, off = base + g * rows + (in ? n : 0);
+        float m = kAttnLow, l = 0.0f;
+#pragma unroll 4
+        for (int p = wave * 4 + g; p < parts; p += waves * 4) {
+            const float* src = part(p) + base + (in ? n : 0);
+            const float om = src[0], ol = src[4 * rows];
+            const float now = __builtin_fmaxf(m, om);
+            l = l * __builtin_amdgcn_exp2f(m - now) + ol * __builtin_amdgcn_exp2f(om - now);
+            m = now;
+        }
+#pragma unroll
+        for (int off2 = 16; off2 < 64; off2 <<= 1) {
+            const float om = __shfl_xor(m, off2, 64), ol = __shfl_xor(l, off2, 64);
+            const float now = __builtin_fmaxf(m, om);
+            l = l * __builtin_amdgcn_exp2f(m - now) + ol * __builtin_amdgcn_exp2f(om - now);
+            m = now;
+        }
+        if (lane < 16) {
             red[wave][0][n] = m;
+            red[wave][1][n] = l;
+        }
         __syncthreads();
+        m = kAttnLow;
         for (int i = 0; i < waves; i++)
             m = __builtin_fmaxf(m, red[i][0][n]);
-        float l = 0.0f;
-        for (int p = wave * 4 + (lane >> 4); p < parts; p += waves * 4) {
-            const float* src = part(p) + t * (D / 4 + 2) * 64 + n;
-            const float g = __builtin_amdgcn_exp2f(src[0] - m);
-            weight[p][n] = g;
-            l += src[64] * g;
-        }
-        l += __shfl_xor(l, 16, 64);
-        l += __shfl_xor(l, 32, 64);
-        if (lane < 16)
-            red[wave][1][n] = l;
-        __syncthreads();
         l = 0.0f;
         for (int i = 0; i < waves; i++)
-            l += red[i][1][n];
-        const int r = row0 + 16 * t + n;
+            l += red[i][1][n] * __builtin_amdgcn_exp2f(red[i][0][n] - m);
+        const int r = tile.row0 + 16 * t + n;
         const int i = r / a.group, head = h * a.group + r - i * a.group;
-        const int64_t token = s.q0 + i;
+        const int64_t token = tile.q0 + i;
         const float scale = l > 0.0f ? vg / l : 0.0f;
-        if (i < s.nq && a.lse && blockIdx.z == 0 && threadIdx.x < 16)
+        if (in && a.lse && blockIdx.z == 0 && threadIdx.x < 16)
             a.lse[token * (a.kv_heads * a.group) + head] =
                 l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
-        const int run = (parts + waves - 1) / waves, p1 = (wave + 1) * run < parts ? (wave + 1) * run : parts;
-        for (int c = blockIdx.z; c < D / 16; c += gridDim.z) {
+        const int runs = waves / pieces, pw = wave / pieces;
+        const int run = (parts + runs - 1) / runs, p1 = (pw + 1) * run < parts ? (pw + 1) * run : parts;
+        for (int c0 = blockIdx.z * pieces; c0 < D / 16; c0 += gridDim.z * pieces) {
+            const int c = c0 + wave % pieces;  // (D / 16 is a multiple of pieces)
             const int k = c / (D / 64), dd = 4 * (c - k * (D / 64));
             float4_t o = (float4_t){0, 0, 0, 0};
 #pragma unroll 4
-            for (int p = wave * run; p < p1; p++) {
-                const float* src = part(p) + (t * (D / 4 + 2) + 2 + 4 * dd + k) * 64 + lane;
-                const float g = weight[p][n];
+            for (int p = pw * run; p < p1; p++) {
+                const float* src = part(p) + off;
+                const float f = __builtin_amdgcn_exp2f(src[0] - m);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    o[j] = __builtin_fmaf(src[4 * j * 64], g, o[j]);
+                    o[j] = __builtin_fmaf(src[(2 + 4 * (dd + j) + k) * 4 * rows], f, o[j]);
             }
-            __syncthreads();  // the last piece's reads of sum are done
-            sum[wave][lane] = o;
-            __syncthreads();
-            if (wave == 0 && i < s.nq) {
-                for (int q = 1; q < waves; q++)
-                    o += sum[q][lane];
-                *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * (lane >> 4) + k) * (D / 16) + dd) =
+            if (runs > 1) {
+                sum[wave][lane] = o;
+                __syncthreads();
+                for (int q = 1; q < runs && pw == 0; q++)
+                    o += sum[wave + q * pieces][lane];
+            }
+            if (pw == 0 && in)
+                *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
                     (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
-            }
+            if (runs > 1)
+                __syncthreads();  // sum is written again
         }
-        __syncthreads();  // weight and red are written again
+        __syncthreads();  // red is written again
     }
 }
 

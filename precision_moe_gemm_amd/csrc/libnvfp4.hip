@@ -217,27 +217,39 @@ int attention_workers(int kv_heads, int head_lanes)
 
 int attention_head_lanes(int kv_heads) { return kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1); }
 
-size_t attention_ws_bytes(int kv_heads, int64_t D)
+// Tiles of `rows` query rows that n tokens in seqs sequences can need.
+int64_t attention_tiles(int64_t n, int64_t group, int64_t seqs, int rows) { return n * group / rows + seqs; }
+
+size_t attention_tiles_bytes(int64_t n, int64_t group, int64_t seqs)
+{
+    return align256((size_t)(1 + attention_tiles(n, group, seqs, 16)) * sizeof(AttnTile));
+}
+
+size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64_t seqs)
 {
     const int hl = attention_head_lanes(kv_heads);
-    // two slots per share and KV head, 16 rows (32 with two row tiles) of D values, m and l
-    return align256((size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float));
+    // two slots per share and KV head, 32 rows of D values, m and l
+    return attention_tiles_bytes(n, q_heads / kv_heads, seqs) +
+           align256((size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float));
 }
 
 template <int D, int NT>
 nvfp4_status launch_attention_rows(const AttnArgs& a, hipStream_t st)
 {
-    const int64_t tiles = a.n * a.group / (16 * NT) + a.seqs;
-    if (tiles > 0x7FFFFFFF || a.kv_heads > 65535)
+    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, 16 * NT);
+    // (units are counted in 31 bits)
+    if ((double)tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) > 2147483647.0 || a.kv_heads > 65535)
         return NVFP4_ERR_UNSUPPORTED;
     const int blocks = a.kv_heads / a.head_lanes;
     attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), kAttnThreads, 0, st>>>(a);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK)
         return s;
-    const int64_t z = std::max<int64_t>(1, std::min<int64_t>(D / 16, 512 / (tiles * a.kv_heads)));
-    const unsigned threads = tiles * a.kv_heads * z >= 512 ? 256 : 1024;
-    attn_combine_kernel<D, NT><<<dim3((unsigned)tiles, a.kv_heads, (unsigned)z), threads, 0, st>>>(a);
+    // many tiles: four waves, each other pieces of the output; few tiles (of
+    // many parts each): 16 waves share the parts of one piece
+    const bool many = tiles * a.kv_heads >= 128;
+    attn_combine_kernel<D, NT><<<dim3((unsigned)tiles, a.kv_heads, many ? 1 : D / 16), many ? 256 : 1024, 0, st>>>(
+        a, many ? 4 : 1);
     return launch_status();
 }
 
@@ -1027,7 +1039,7 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         // T query rows, k query heads, E KV heads, H = head_dim, I = sequences
         if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
             return 0;
-        return attention_ws_bytes(E, H);
+        return attention_ws_bytes(T, k, E, H, I);
     }
     return 0;
 }
@@ -2191,7 +2203,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.out = (uint16_t*)out;
     a.ld_out = ld_out;
     a.lse = lse;
-    a.partial = (float*)ws;
+    a.tiles = (AttnTile*)ws;
+    a.partial = (float*)((uint8_t*)ws + attention_tiles_bytes(n, a.group, seqs));
     if (!cu_q)
         max_q = 1;
     nvfp4_status s = D == 64    ? launch_attention<64>(a, max_q, S(stream))
