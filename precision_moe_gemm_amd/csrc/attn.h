@@ -64,7 +64,10 @@ struct AttnArgs {
     float* partial;          // what shares leave of tiles that they hold a part of
 };
 
-constexpr int kAttnThreads = 256;
+// Waves of a row workgroup: 8, or 4 where their joining space would pass the
+// shared memory.
+template <int D, int NT>
+constexpr int attn_waves() { return D * NT <= 256 ? 8 : 4; }
 typedef __attribute__((address_space(3))) void* attn_lds_t;
 constexpr int kAttnStep = 32;            // tokens of one step
 constexpr float kAttnLow = -1e30f;       // running maximum of a row that has seen nothing
@@ -594,14 +597,14 @@ struct AttnWave {
 
 // Joins the waves that walked different tokens for the same head: wave w
 // holds head lane w % hl and token lane w / hl.  buf: D / 4 + 2 floats x 64
-// lanes x NT per writing wave, two of them at most.  Afterwards token lane 0
-// holds the whole.
+// lanes x NT per writing wave, half the waves at most.  Afterwards token lane
+// 0 holds the whole.
 template <int D, int NT>
 NVFP4_DEV void attn_join(AttnWave<D, NT>& w, int hl, int wave, float* buf)
 {
     constexpr int kRow = D / 4 + 2;
     const int tl = wave / hl, lane = threadIdx.x & 63;
-    for (int s = (kAttnThreads / 64) / hl / 2; s > 0; s >>= 1) {
+    for (int s = attn_waves<D, NT>() / hl / 2; s > 0; s >>= 1) {
         __syncthreads();
         if (tl >= s && tl < 2 * s) {
             float* b = buf + (wave - s * hl) * (kRow * NT * 64) + lane;
@@ -707,15 +710,16 @@ struct AttnTile {
 // A workgroup holds head_lanes KV heads side by side, which lie next to each
 // other in memory, and (waves / head_lanes) runs of the tokens.
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, D * NT <= 64 ? 4 : (D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1)))
+__global__ void __launch_bounds__((64 * attn_waves<D, NT>()), (D * NT <= 64 ? 4 : (D * NT <= 256 ? 2 : 1)))
 attn_rows_kernel(AttnArgs a)
 {
     // the waves' copies of K and V; between walks the space of joined waves
-    constexpr int kStages = 4 * attn_stage<D>(), kJoin = 2 * attn_part<D, NT>() * 4;
+    constexpr int kWaves = attn_waves<D, NT>(), kStages = kWaves * attn_stage<D>();
+    constexpr int kJoin = kWaves / 2 * attn_part<D, NT>() * 4;
     __shared__ __attribute__((aligned(16))) uint8_t bufk[kStages > kJoin ? kStages : kJoin];
     __shared__ __attribute__((aligned(16))) uint8_t bufv[kStages];
     const int wave = uniform((int)(threadIdx.x >> 6));
-    const int hl = a.head_lanes, tls = (kAttnThreads / 64) / hl;
+    const int hl = a.head_lanes, tls = kWaves / hl;
     // workgroups go to the 8 XCDs in turn: the head blocks of one share go to
     // the same one, whose L2 then holds the lines that they share
     const int blocks = a.kv_heads / hl;
@@ -795,100 +799,85 @@ attn_rows_kernel(AttnArgs a)
 }
 
 // Joins what the shares left of one tile of rows (blockIdx.x) for one KV head
-// (blockIdx.y), in the order of the tokens: max and sum over all parts first,
-// then the sums of o with the weights exp2(m - max).  A piece of 4 output
-// elements per lane at a time: `pieces` waves take different pieces, the
-// others (few tiles with many parts each) different runs of the parts.
+// (blockIdx.y), in the order of the tokens, with the running maximum and sum
+// of the walk.  A wave holds a piece of 4 output elements per lane:
+// `pieces` waves take different pieces, the others (few tiles with many
+// parts each) different runs of the parts, joined through shared memory.
+// What it takes is the latency of three dependent reads and the launch.
 template <int D, int NT>
 __global__ void __launch_bounds__(1024)
 attn_combine_kernel(AttnArgs a, int pieces)
 {
-    __shared__ float red[16][2][16];
     __shared__ float4_t sum[16][64];
+    __shared__ float2_t red[16][64];
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = uniform((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
-    if ((int)blockIdx.x >= a.tiles[0].parts)
-        return;
+    // (both read before the first test, so that their latencies overlap)
+    const int tiles = a.tiles[0].parts;
     const AttnTile tile = a.tiles[1 + blockIdx.x];
+    const float vg = *a.v_global;
     const int parts = uniform(tile.parts), w0 = uniform(tile.first);
-    if (parts == 1)
-        return;  // one share held the whole tile
+    if ((int)blockIdx.x >= tiles || parts == 1)
+        return;  // no such tile, or one share held the whole of it
     const int hl = a.head_lanes, blocks = a.kv_heads / hl;
     const int h = blockIdx.y, hb = h / hl;
-    const float vg = *a.v_global;
     // part p: the share w0 + p, slot 1 of the first, slot 0 of the others
     auto part = [&](int p) {
         return a.partial + (((int64_t)(w0 + p) * blocks + hb) * 2 + (p == 0)) * hl * attn_part<D, NT>() +
                (h - hb * hl) * attn_part<D, NT>();
     };
+    const int runs = waves / pieces, pw = wave / pieces;
+    const int run = (parts + runs - 1) / runs, p0 = pw * run, p1 = p0 + run < parts ? p0 + run : parts;
 #pragma unroll 1
     for (int t = 0; t < NT; t++) {
-        const int left = tile.nq * a.group - tile.row0 - 16 * t, rows = attn_part_rows(left);
+        const int rows = attn_part_rows(tile.nq * a.group - tile.row0 - 16 * t);
         if (rows == 0)
             break;
         const bool in = n < rows;
-        const int base = t * (D / 4 + 2) * 64, off = base + g * rows + (in ? n : 0);
-        float m = kAttnLow, l = 0.0f;
-#pragma unroll 4
-        for (int p = wave * 4 + g; p < parts; p += waves * 4) {
-            const float* src = part(p) + base + (in ? n : 0);
-            const float om = src[0], ol = src[4 * rows];
-            const float now = __builtin_fmaxf(m, om);
-            l = l * __builtin_amdgcn_exp2f(m - now) + ol * __builtin_amdgcn_exp2f(om - now);
-            m = now;
-        }
-#pragma unroll
-        for (int off2 = 16; off2 < 64; off2 <<= 1) {
-            const float om = __shfl_xor(m, off2, 64), ol = __shfl_xor(l, off2, 64);
-            const float now = __builtin_fmaxf(m, om);
-            l = l * __builtin_amdgcn_exp2f(m - now) + ol * __builtin_amdgcn_exp2f(om - now);
-            m = now;
-        }
-        if (lane < 16) {
-            red[wave][0][n] = m;
-            red[wave][1][n] = l;
-        }
-        __syncthreads();
-        m = kAttnLow;
-        for (int i = 0; i < waves; i++)
-            m = __builtin_fmaxf(m, red[i][0][n]);
-        l = 0.0f;
-        for (int i = 0; i < waves; i++)
-            l += red[i][1][n] * __builtin_amdgcn_exp2f(red[i][0][n] - m);
+        const int off = t * (D / 4 + 2) * 64 + g * rows + (in ? n : 0);
         const int r = tile.row0 + 16 * t + n;
         const int i = r / a.group, head = h * a.group + r - i * a.group;
         const int64_t token = tile.q0 + i;
-        const float scale = l > 0.0f ? vg / l : 0.0f;
-        if (in && a.lse && blockIdx.z == 0 && threadIdx.x < 16)
-            a.lse[token * (a.kv_heads * a.group) + head] =
-                l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
-        const int runs = waves / pieces, pw = wave / pieces;
-        const int run = (parts + runs - 1) / runs, p1 = (pw + 1) * run < parts ? (pw + 1) * run : parts;
         for (int c0 = blockIdx.z * pieces; c0 < D / 16; c0 += gridDim.z * pieces) {
             const int c = c0 + wave % pieces;  // (D / 16 is a multiple of pieces)
             const int k = c / (D / 64), dd = 4 * (c - k * (D / 64));
+            float m = kAttnLow, l = 0.0f;
             float4_t o = (float4_t){0, 0, 0, 0};
+            auto join = [&](float om, float ol, float4_t oo) {
+                const float now = __builtin_fmaxf(m, om);
+                const float f = __builtin_amdgcn_exp2f(m - now), q = __builtin_amdgcn_exp2f(om - now);
+                l = l * f + ol * q;
+                o = o * f + oo * q;
+                m = now;
+            };
 #pragma unroll 4
-            for (int p = pw * run; p < p1; p++) {
+            for (int p = p0; p < p1; p++) {
                 const float* src = part(p) + off;
-                const float f = __builtin_amdgcn_exp2f(src[0] - m);
+                float4_t oo;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    o[j] = __builtin_fmaf(src[(2 + 4 * (dd + j) + k) * 4 * rows], f, o[j]);
+                    oo[j] = src[(2 + 4 * (dd + j) + k) * 4 * rows];
+                join(src[0], src[4 * rows], oo);
             }
             if (runs > 1) {
                 sum[wave][lane] = o;
+                red[wave][lane] = (float2_t){m, l};
                 __syncthreads();
-                for (int q = 1; q < runs && pw == 0; q++)
-                    o += sum[wave + q * pieces][lane];
+                for (int q = 1; q < runs && pw == 0; q++) {
+                    const float2_t ml = red[wave + q * pieces][lane];
+                    join(ml.x, ml.y, sum[wave + q * pieces][lane]);
+                }
+                __syncthreads();  // sum and red are written again
             }
-            if (pw == 0 && in)
-                *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
-                    (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
-            if (runs > 1)
-                __syncthreads();  // sum is written again
+            if (pw != 0 || !in)
+                continue;
+            const float scale = l > 0.0f ? vg / l : 0.0f;
+            *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
+                (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
+            if (a.lse && c == 0 && g == 0)
+                a.lse[token * (a.kv_heads * a.group) + head] =
+                    l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
         }
-        __syncthreads();  // red is written again
     }
 }
 

@@ -212,7 +212,7 @@ void launch_kv_append(const AppendArgs& a, hipStream_t st)
 // per CU) divided over the blocks of KV heads, a multiple of 8.
 int attention_workers(int kv_heads, int head_lanes)
 {
-    return std::max(8, 512 / (kv_heads / head_lanes) / 8 * 8);
+    return std::max(8, 256 / (kv_heads / head_lanes) / 8 * 8);
 }
 
 int attention_head_lanes(int kv_heads) { return kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1); }
@@ -241,7 +241,7 @@ nvfp4_status launch_attention_rows(const AttnArgs& a, hipStream_t st)
     if ((double)tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) > 2147483647.0 || a.kv_heads > 65535)
         return NVFP4_ERR_UNSUPPORTED;
     const int blocks = a.kv_heads / a.head_lanes;
-    attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), kAttnThreads, 0, st>>>(a);
+    attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), 64 * attn_waves<D, NT>(), 0, st>>>(a);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK)
         return s;
