@@ -31,6 +31,8 @@
 // product gives group g tokens 4i + g of both tiles; its output row m of MFMA
 // dd is element m D / 16 + dd, so a lane needs a contiguous piece of a V row.
 #pragma once
+#include <type_traits>
+
 #include "common.h"
 #include "gemm.h"
 
@@ -52,6 +54,8 @@ struct AttnArgs {
     int64_t num_pages;       // pages in the cache
     int64_t n;               // rows of q
     int seqs, pages, page;   // page: tokens of a page (a multiple of 16)
+    int page_shift;          // floor((t / 16) / (page / 16)) = (t / 16) * page_mul >> (32 + page_shift)
+    uint32_t page_mul;       // (0: page is 16)
     int kv_heads, group;     // group: query heads per KV head
     float scale_log2;        // scale * log2(e)
     int causal, window;
@@ -79,6 +83,13 @@ constexpr float kAttnLift = 7.0f;        // p is held times 2^7, at most 2^15 (f
 struct AttnSeq {
     int q0, nq, kv;
 };
+
+// The page of token t >= 0 of a sequence.
+NVFP4_DEV int attn_page(const AttnArgs& a, int t)
+{
+    const uint32_t n = (uint32_t)t >> 4;
+    return (int)(a.page_mul ? __umulhi(n, a.page_mul) >> a.page_shift : n);
+}
 
 // The value of a variable that is the same in all lanes, held in a scalar
 // register: addresses and branches that depend on it are then scalar too.
@@ -878,6 +889,419 @@ attn_combine_kernel(AttnArgs a, int pieces)
                 a.lse[token * (a.kv_heads * a.group) + head] =
                     l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
         }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many query rows per sequence (chunks, prompts): the time is the two
+// products.  A workgroup of NW waves takes a tile of 32 NW query rows of one
+// sequence and KV head, each wave 32 of them, and walks the tokens in blocks
+// of 64.  A block of K and V is decoded to f16 once for all waves, into one of
+// two buffers in shared memory while the other is multiplied: decoding it in
+// every wave took 680 VALU cycles a wave for 512 cycles of products (D = 128).
+//
+// v_mfma_f32_32x32x16_f16 (A: row l % 32, B: column l % 32, both elements
+// 8 (l / 32) .. + 8 of the contraction; output: column l % 32, rows
+// 8 (i / 4) + 4 (l / 32) + i % 4 for register i of lane l), transposed as in
+// the row kernel: S^T = K Q^T, O^T = V^T P^T, and eight registers of S^T are
+// a lane's share of P^T for 16 tokens.  They are tokens 4 e .. 4 e + 3 and
+// 8 + 4 e .. + 3 of the 16 (e = l / 32), so V^T rows are kept with their tokens
+// in that order: token t of 16 at place t % 4 + 4 (t / 8) + 8 (t / 4 % 2).
+// ---------------------------------------------------------------------------
+constexpr int kTileTok = 64;
+
+// Place (in 16-byte chunks) of chunk c of row r in the f16 tiles, rows of C
+// chunks: the XOR spreads both the operand reads (32 consecutive rows, one
+// chunk) and the writes over the banks.
+template <int C>
+NVFP4_DEV int tile_chunk(int r, int c)
+{
+    return r * C + (c ^ (C >= 16 ? r & 15 : ((r >> 1) ^ (r >> 4)) & 7));
+}
+
+// f(integral_constant<int, B>), ..., f(integral_constant<int, E - 1>)
+template <int B, int E, class F>
+NVFP4_DEV void for_range(F f)
+{
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        for_range<B + 1, E>(f);
+    }
+}
+
+NVFP4_DEV float16_t mfma32(half8_t a, half8_t b, float16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// What a thread of NT holds of a block on its way: kK elements of one token
+// of K, and kV elements of four tokens of V.
+template <int D, int NT>
+struct TileRaw {
+    static constexpr int kK = kTileTok * D / NT, kV = kK / 4;
+    static constexpr int kUnits = kK / 8;  // pieces of decoding of K (8 elements each) and of V (2 of each token)
+    uint32_t kc[kK / 8];
+    uint32_t ks;
+    uint32_t vc[4][kV > 8 ? kV / 8 : 1];
+    uint32_t vs[4];
+    bool ok;  // K's page is one of the cache
+};
+
+// N bytes (1, 2, 4, 8, 16 or 32) from src into dwords.
+template <int N>
+NVFP4_DEV void load_bytes(const uint8_t* src, uint32_t* w)
+{
+    if constexpr (N == 1) {
+        w[0] = *src;
+    } else if constexpr (N == 2) {
+        w[0] = *(const uint16_t*)src;
+    } else if constexpr (N == 4) {
+        w[0] = *(const uint32_t*)src;
+    } else if constexpr (N == 8) {
+        const u32x2 v = *(const u32x2*)src;
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 16; i++) {
+            const u32x4 v = ((const u32x4*)src)[i];
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                w[4 * i + j] = v[j];
+        }
+    }
+}
+
+// Byte I of an interleaved dword (two tokens' codes of one element) under the two tokens' scales.
+template <int I>
+NVFP4_DEV uint32_t decode_pair(uint32_t w, half2_t s)
+{
+    return __builtin_bit_cast(uint32_t, FP4_TO_F16X2_256(w, I) * s);
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__((64 * NW), (D == 256 ? 1 : 2))
+attn_tile_kernel(AttnArgs a)
+{
+    constexpr int NT = 64 * NW, ROWS = 32 * NW;
+    constexpr int KC = D / 8;  // chunks of a K row
+    typedef TileRaw<D, NT> Raw;
+    __shared__ __attribute__((aligned(16))) u32x4 lk[2][kTileTok * KC];
+    __shared__ __attribute__((aligned(16))) u32x4 lv[2][D * 8];
+    __shared__ __attribute__((aligned(16))) int lok[2][4];  // which 16 tokens lie in a page of the cache
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, e = lane >> 5;
+    const int wave = uniform(tid >> 6);
+    // ---- the tile: heavy ones first (causal tiles grow towards the end)
+    const int h = blockIdx.x % a.kv_heads;
+    const int split = blockIdx.y;
+    auto count = [&](int b) {
+        const AttnSeq s = attn_seq(a, b);
+        return AttnCount{(s.nq * a.group + ROWS - 1) / ROWS, 1};
+    };
+    const AttnScan scan = attn_scan(a.seqs, count);
+    const int slot = blockIdx.x / a.kv_heads;
+    if (gridDim.y > 1 && blockIdx.x == 0 && split == 0 && tid == 0)
+        a.tiles[0].parts = scan.units;
+    if (slot >= scan.units)
+        return;
+    const int tile_no = scan.units - 1 - slot;
+    const AttnFound f = attn_find(scan, a.seqs, tile_no, count);
+    const AttnSeq s = attn_seq_uniform(a, f.seq);
+    const int row0 = f.at * ROWS;
+    int lo0, hi0, lo1, hi1;  // tokens of the tile's first and last row
+    const int last = (row0 + ROWS - 1) / a.group;
+    attn_limits(a, s, row0 / a.group, &lo0, &hi0);
+    attn_limits(a, s, last < s.nq ? last : s.nq - 1, &lo1, &hi1);
+    // ---- this split's blocks [b0, b1) of the tile's
+    int b0 = lo0 / kTileTok, b1 = hi1 > lo0 ? (hi1 + kTileTok - 1) / kTileTok : b0;
+    if (gridDim.y > 1) {
+        const int n = b1 - b0, per = (n + (int)gridDim.y - 1) / (int)gridDim.y;
+        const int base = b0;
+        b0 = base + split * per < b1 ? base + split * per : b1;
+        b1 = b0 + per < b1 ? b0 + per : b1;
+    }
+    // ---- queries: lane's row (column of the products) and its limits
+    const int r = row0 + 32 * wave + col;
+    const int qi = r / a.group, hh = r - qi * a.group;
+    const bool in = qi < s.nq;
+    int start = 0, end = 0;
+    if (in)
+        attn_limits(a, s, qi, &start, &end);
+    half8_t q[D / 16];
+    float c1;
+    {
+        const uint16_t* src = a.q + (int64_t)(s.q0 + (in ? qi : 0)) * a.ld_q + (int64_t)(h * a.group + hh) * D + 8 * e;
+        u32x4 w[D / 16];
+        uint32_t am = 0;
+#pragma unroll
+        for (int c = 0; c < D / 16; c++) {
+            w[c] = (u32x4){0, 0, 0, 0};
+            if (in)
+                w[c] = *(const u32x4*)(src + 16 * c);
+            am = umax_u32(am, absmax_bits8(w[c]));
+        }
+        am = umax_u32(am, (uint32_t)__shfl_xor((int)am, 32, 64));
+        const int ex = am ? __builtin_amdgcn_frexp_expf(__uint_as_float(am << 16)) - 1 : 0;
+        c1 = __builtin_fmaxf(__builtin_ldexpf(a.scale_log2 * *a.k_global, ex), 1e-37f);
+#pragma unroll
+        for (int c = 0; c < D / 16; c++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                q[c][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[c][j]), -ex);
+                q[c][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[c][j]), -ex);
+            }
+    }
+    // ---- staging: the thread's elements of K (token kt, elements kd .. + kK)
+    // and of V (tokens 4 vt .. + 4, elements vd .. + kV)
+    const int32_t* table = a.table + f.seq * a.ld_table;
+    const int first_page = attn_page(a, lo0), last_page = attn_page(a, hi1 > 0 ? hi1 - 1 : 0);
+    const int64_t crow = (int64_t)a.kv_heads * (D / 2), srow = (int64_t)a.kv_heads * (D / 16);
+    const int kt = tid / (D / Raw::kK), kd = tid % (D / Raw::kK) * Raw::kK;
+    const int vt = tid / (D / Raw::kV), vd = tid % (D / Raw::kV) * Raw::kV;
+    const uint8_t* const k_codes = a.k_packed + h * (D / 2) + kd / 2;
+    const uint8_t* const k_scales = a.k_scales + h * (D / 16) + kd / 16;
+    const uint8_t* const v_codes = a.v_packed + h * (D / 2) + vd / 2;
+    const uint8_t* const v_scales = a.v_scales + h * (D / 16) + vd / 16;
+    Raw raw;
+    int kp = 0, vp = 0;  // the pages of the next block's tokens
+    bool bad = false;
+    // the entry of the page of token t (past the end: the last page, masked)
+    auto entry = [&](int t) {
+        const int i = attn_page(a, t);
+        return table[i < last_page ? i : last_page];
+    };
+    auto pages = [&](int blk) {
+        kp = entry(blk * kTileTok + kt);
+        vp = entry(blk * kTileTok + 4 * vt);
+    };
+    // the first row of token t in the cache; a page that is none of the cache's: page 0
+    auto row_of = [&](int page, int t, bool* ok) {
+        const int i = attn_page(a, t);
+        *ok = page >= 0 && page < a.num_pages;
+        // (a page with no token that a row sees may hold anything)
+        bad |= !*ok && t < hi1 && i >= first_page;
+        return (int64_t)(*ok ? page : 0) * a.page + (t - i * a.page);
+    };
+    auto load = [&](int blk) {
+        const int64_t k = row_of(kp, blk * kTileTok + kt, &raw.ok);
+        load_bytes<Raw::kK / 2>(k_codes + k * crow, raw.kc);
+        load_bytes<(Raw::kK > 16 ? Raw::kK / 16 : 1)>(k_scales + k * srow, &raw.ks);
+        bool ok;
+        const int64_t v = row_of(vp, blk * kTileTok + 4 * vt, &ok);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            load_bytes<Raw::kV / 2>(v_codes + (v + i) * crow, raw.vc[i]);
+            raw.vs[i] = v_scales[(v + i) * srow];
+        }
+    };
+    // V's codes with two tokens side by side: byte i of even / odd: elements 2i / 2i + 1
+    uint32_t even[2][Raw::kV > 8 ? Raw::kV / 8 : 1], odd[2][Raw::kV > 8 ? Raw::kV / 8 : 1];
+    half2_t vsc[2];
+    auto interleave = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+#pragma unroll
+            for (int w = 0; w < (Raw::kV > 8 ? Raw::kV / 8 : 1); w++) {
+                const uint32_t x = raw.vc[2 * i][w], y = raw.vc[2 * i + 1][w];
+                even[i][w] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+                odd[i][w] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+            }
+            vsc[i] = scale_pair(raw.vs[2 * i], raw.vs[2 * i + 1]);
+        }
+        if (kd == 0 && (kt & 15) == 0)
+            lok[buf][kt >> 4] = raw.ok;
+    };
+    // tokens 4 vt .. + 4 of the block: 8 bytes at place 8 (vt % 2) + 4 (vt / 2 % 2) of their 16
+    const int vchunk = 2 * (vt >> 2) + (vt & 1), vpart = (vt >> 1) & 1;
+    // piece U of decoding the block in raw into buffer buf
+    auto decode = [&](int buf, auto unit) {
+        constexpr int U = decltype(unit)::value;
+        const uint32_t b = raw.ks >> (8 * (U >> 1));
+        lk[buf][tile_chunk<KC>(kt, kd / 8 + U)] = __builtin_bit_cast(u32x4, decode_row8(raw.kc[U], scale_pair(b, b)));
+        u32x2* dst = (u32x2*)lv[buf] + vpart;
+        constexpr int W = U / 4, I = U % 4;
+        dst[2 * tile_chunk<8>(vd + 2 * U, vchunk)] =
+            (u32x2){decode_pair<I>(even[0][W], vsc[0]), decode_pair<I>(even[1][W], vsc[1])};
+        dst[2 * tile_chunk<8>(vd + 2 * U + 1, vchunk)] =
+            (u32x2){decode_pair<I>(odd[0][W], vsc[0]), decode_pair<I>(odd[1][W], vsc[1])};
+    };
+    auto decode_all = [&](int buf) {
+        interleave(buf);
+        for_range<0, Raw::kUnits>([&](auto u) { decode(buf, u); });
+    };
+
+    float16_t o[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            o[d][i] = 0.0f;
+    float m = kAttnLow, l = 0.0f;
+    if (b0 < b1) {
+        pages(b0);
+        load(b0);
+        pages(b0 + 1);
+        decode_all(0);
+        load(b0 + 1);
+        pages(b0 + 2);
+    }
+    // (past the end the loads go to the last page again and are not used)
+    for (int blk = b0; blk < b1; blk++) {
+        const int buf = (blk - b0) & 1;
+        __syncthreads();  // buffer `buf` is written, and nobody reads the other any more
+        const int t0 = blk * kTileTok;
+        const u32x4 ok = *(const u32x4*)lok[buf];
+        // ---- S^T, and between its products the decoding of the next block
+        interleave(buf ^ 1);
+        float16_t sc[2];
+#pragma unroll
+        for (int p = 0; p < 2; p++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                sc[p][i] = 0.0f;
+        for_range<0, D / 16>([&](auto ci) {
+            constexpr int c = decltype(ci)::value, per = D / 16 / Raw::kUnits;  // (kUnits <= D / 16)
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+                sc[p] = mfma32(__builtin_bit_cast(half8_t, lk[buf][tile_chunk<KC>(32 * p + col, 2 * c + e)]), q[c], sc[p]);
+            if constexpr (c % per == per - 1)
+                decode(buf ^ 1, std::integral_constant<int, c / per>{});
+        });
+        load(blk + 2);
+        pages(blk + 3);
+        if (!(t0 >= lo1 && t0 + kTileTok <= hi0 && (ok.x & ok.y & ok.z & ok.w) != 0)) {
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int tok = t0 + 32 * p + 8 * (i >> 2) + 4 * e + (i & 3);
+                    const bool seen = tok >= start && tok < end && ok[2 * p + (i >> 3)] != 0;
+                    sc[p][i] = seen ? sc[p][i] : -__builtin_inff();
+                }
+        }
+        float top = sc[0][0];
+#pragma unroll
+        for (int i = 1; i < 32; i++)
+            top = __builtin_fmaxf(top, sc[i >> 4][i & 15]);
+        top *= c1;
+        if (__any(top > m + kAttnLazy)) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+            const float now = __builtin_fmaxf(m, top);
+            const float g = __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            l *= g;
+#pragma unroll
+            for (int d = 0; d < D / 32; d++)
+                o[d] *= g;
+        }
+        const float lift = kAttnLift - m;
+        // ---- P^T of 16 tokens, and O^T += V^T P^T of the 16 before
+        half8_t pt[4];
+        auto weigh = [&](int k) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k >> 1][8 * (k & 1) + i], c1, lift));
+            l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                pt[k][i] = (_Float16)x[i];
+        };
+        weigh(0);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (k < 3)
+                weigh(k + 1);
+#pragma unroll
+            for (int d = 0; d < D / 32; d++)
+                o[d] = mfma32(__builtin_bit_cast(half8_t, lv[buf][tile_chunk<8>(32 * d + col, 2 * k + e)]), pt[k], o[d]);
+        }
+    }
+    if (bad)
+        raise_error(NVFP4_ERR_RANGE);
+    l += __shfl_xor(l, 32, 64);
+    const int head = h * a.group + hh;
+    const int64_t token = s.q0 + qi;
+    if (gridDim.y > 1) {
+        // (m, l, o) of this split: [tile][kv head][split][row][D + 4]
+        if (split == 0 && h == 0 && tid == 0)
+            a.tiles[1 + tile_no] = AttnTile{0, (int)gridDim.y, s.q0, s.nq, row0};
+        if (in) {
+            float* dst = a.partial + ((((int64_t)tile_no * a.kv_heads + h) * gridDim.y + split) * ROWS + 32 * wave + col) * (D + 4);
+            if (e == 0) {
+                dst[D] = m;
+                dst[D + 1] = l;
+            }
+#pragma unroll
+            for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    *(float4_t*)(dst + 32 * d + 8 * i + 4 * e) =
+                        (float4_t){o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        }
+        return;
+    }
+    if (!in)
+        return;
+    const float g = l > 0.0f ? *a.v_global / l : 0.0f;
+    uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + 4 * e;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            *(u32x2*)(dst + 32 * d + 8 * i) = (u32x2){pack_bf16x2(o[d][4 * i] * g, o[d][4 * i + 1] * g),
+                                                      pack_bf16x2(o[d][4 * i + 2] * g, o[d][4 * i + 3] * g)};
+    if (a.lse && e == 0)
+        a.lse[token * (a.kv_heads * a.group) + head] =
+            l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+}
+
+// Joins the splits of a tile of ROWS rows (blockIdx.x) and KV head
+// (blockIdx.y): a wave a row at a time.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256)
+attn_tile_combine_kernel(AttnArgs a)
+{
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int tiles = a.tiles[0].parts;
+    const AttnTile tile = a.tiles[1 + blockIdx.x];
+    const float vg = *a.v_global;
+    if ((int)blockIdx.x >= tiles)
+        return;
+    const int h = blockIdx.y, parts = uniform(tile.parts);
+    constexpr int V = D / 64;  // elements per lane
+    for (int row = blockIdx.z * 4 + wave; row < ROWS; row += gridDim.z * 4) {
+        const int r = tile.row0 + row, i = r / a.group, head = h * a.group + r - i * a.group;
+        if (i >= tile.nq)
+            break;
+        const float* src = a.partial + (((int64_t)blockIdx.x * a.kv_heads + h) * parts * ROWS + row) * (D + 4);
+        float m = kAttnLow, l = 0.0f, o[V];
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            o[j] = 0.0f;
+#pragma unroll 4
+        for (int p = 0; p < parts; p++) {
+            const float* x = src + (int64_t)p * ROWS * (D + 4);
+            const float om = x[D], ol = x[D + 1], now = __builtin_fmaxf(m, om);
+            const float f = __builtin_amdgcn_exp2f(m - now), g = __builtin_amdgcn_exp2f(om - now);
+            l = l * f + ol * g;
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                o[j] = o[j] * f + x[lane * V + j] * g;
+            m = now;
+        }
+        const int64_t token = tile.q0 + i;
+        const float scale = l > 0.0f ? vg / l : 0.0f;
+        uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + lane * V;
+        if constexpr (V == 1)
+            *dst = f32_to_bf16(o[0] * scale);
+        else
+#pragma unroll
+            for (int j = 0; j < V; j += 2)
+                *(uint32_t*)(dst + j) = pack_bf16x2(o[j] * scale, o[j + 1] * scale);
+        if (a.lse && lane == 0)
+            a.lse[token * (a.kv_heads * a.group) + head] =
+                l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
     }
 }
 

@@ -217,20 +217,38 @@ int attention_workers(int kv_heads, int head_lanes)
 
 int attention_head_lanes(int kv_heads) { return kv_heads % 4 == 0 ? 4 : (kv_heads % 2 == 0 ? 2 : 1); }
 
-// Tiles of `rows` query rows that n tokens in seqs sequences can need.
-int64_t attention_tiles(int64_t n, int64_t group, int64_t seqs, int rows) { return n * group / rows + seqs; }
+// Tiles of `rows` query rows that n tokens in seqs sequences can need (each
+// sequence's last one partly filled).
+int64_t attention_tiles(int64_t n, int64_t group, int64_t seqs, int rows)
+{
+    return (n * group + std::min(n, seqs) * (rows - 1)) / rows;
+}
 
 size_t attention_tiles_bytes(int64_t n, int64_t group, int64_t seqs)
 {
     return align256((size_t)(1 + attention_tiles(n, group, seqs, 16)) * sizeof(AttnTile));
 }
 
+// Splits of the tile kernel's token range: about one workgroup per CU, when
+// there are fewer tiles than that.
+int64_t attention_tile_splits(int64_t tiles, int kv_heads)
+{
+    return std::max<int64_t>(1, 256 / std::max<int64_t>(1, tiles * kv_heads));
+}
+
 size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64_t seqs)
 {
     const int hl = attention_head_lanes(kv_heads);
-    // two slots per share and KV head, 32 rows of D values, m and l
-    return attention_tiles_bytes(n, q_heads / kv_heads, seqs) +
-           align256((size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float));
+    // row kernel: two slots per share and KV head, 32 rows of D values, m and l
+    size_t part = (size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float);
+    // tile kernel: every split of every tile, its rows of D + 4 values
+    for (int rows = 128; rows <= 256; rows *= 2) {
+        const int64_t tiles = attention_tiles(n, q_heads / kv_heads, seqs, rows);
+        const int64_t splits = attention_tile_splits(tiles, kv_heads);
+        if (splits > 1)
+            part = std::max(part, (size_t)(tiles * kv_heads * splits * rows * (D + 4)) * sizeof(float));
+    }
+    return attention_tiles_bytes(n, q_heads / kv_heads, seqs) + align256(part);
 }
 
 template <int D, int NT>
@@ -253,6 +271,23 @@ nvfp4_status launch_attention_rows(const AttnArgs& a, hipStream_t st)
     return launch_status();
 }
 
+template <int D, int NW>
+nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
+{
+    constexpr int ROWS = 32 * NW;
+    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, ROWS);
+    if (tiles * a.kv_heads > 0x7FFFFFFF || a.kv_heads > 65535)
+        return NVFP4_ERR_UNSUPPORTED;
+    const int64_t splits = std::min(attention_tile_splits(tiles, a.kv_heads),
+                                    std::max<int64_t>(1, (int64_t)a.pages * a.page / (4 * kTileTok)));
+    attn_tile_kernel<D, NW><<<dim3((unsigned)(tiles * a.kv_heads), (unsigned)splits), 64 * NW, 0, st>>>(a);
+    nvfp4_status s = launch_status();
+    if (s != NVFP4_OK || splits == 1)
+        return s;
+    attn_tile_combine_kernel<D, ROWS><<<dim3((unsigned)tiles, a.kv_heads, 8), 256, 0, st>>>(a);
+    return launch_status();
+}
+
 template <int D>
 nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
 {
@@ -260,7 +295,12 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
     a.workers = attention_workers(a.kv_heads, a.head_lanes);
     if (max_q * a.group <= 16)
         return launch_attention_rows<D, 1>(a, st);
-    return launch_attention_rows<D, 2>(a, st);
+    if (max_q * a.group <= 32)
+        return launch_attention_rows<D, 2>(a, st);
+    if (D == 256 || max_q * a.group <= 128)
+        return launch_attention_tiles<D, 4>(a, st);
+    if constexpr (D < 256)
+        return launch_attention_tiles<D, 8>(a, st);
 }
 
 // RMS norm: 1024-thread workgroups, up to 8 chunks of 8 elements per thread.
@@ -2195,6 +2235,13 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.seqs = seqs;
     a.pages = pages_per_seq;
     a.page = page_size;
+    if (page_size > 16) {
+        // d = page / 16 in (2^s, 2^(s+1)], mul = ceil(2^(32+s) / d): exact for t / 16 < 2^27
+        const uint64_t d = page_size / 16;
+        while ((2ull << a.page_shift) < d)
+            a.page_shift++;
+        a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
+    }
     a.kv_heads = kv_heads;
     a.group = q_heads / kv_heads;
     a.scale_log2 = scale * 1.44269504089f;
