@@ -54,8 +54,8 @@ struct AttnArgs {
     int64_t num_pages;       // pages in the cache
     int64_t n;               // rows of q
     int seqs, pages, page;   // page: tokens of a page (a multiple of 16)
-    int page_shift;          // floor((t / 16) / (page / 16)) = (t / 16) * page_mul >> (32 + page_shift)
-    uint32_t page_mul;       // (0: page is 16)
+    int page_shift;          // t / page = (t / 8) * page_mul >> (32 + page_shift)
+    uint32_t page_mul;
     int kv_heads, group;     // group: query heads per KV head
     float scale_log2;        // scale * log2(e)
     int causal, window;
@@ -87,8 +87,7 @@ struct AttnSeq {
 // The page of token t >= 0 of a sequence.
 NVFP4_DEV int attn_page(const AttnArgs& a, int t)
 {
-    const uint32_t n = (uint32_t)t >> 4;
-    return (int)(a.page_mul ? __umulhi(n, a.page_mul) >> a.page_shift : n);
+    return (int)(__umulhi((uint32_t)t >> 3, a.page_mul) >> a.page_shift);
 }
 
 // The value of a variable that is the same in all lanes, held in a scalar
@@ -979,6 +978,31 @@ NVFP4_DEV uint32_t decode_pair(uint32_t w, half2_t s)
     return __builtin_bit_cast(uint32_t, FP4_TO_F16X2_256(w, I) * s);
 }
 
+// o *= f for accumulators that fill the accumulation registers (D = 256: 128 of
+// a wave's 512 registers).  Written as a plain product under the rare branch
+// that grows the maximum, it made the compiler move all 128 to the other half
+// of the register file and back in every block (128 moves of 4 cycles against
+// 2062 of products); the constraints keep them where the products want them.
+// The compiler does not see these moves, so the waits that a product (16
+// passes) asks for before its result is read, and a move before its result is
+// an operand, are written out.
+template <int N>
+NVFP4_DEV void scale_acc(float16_t (&o)[N], float f)
+{
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int d = 0; d < N; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            float x;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(o[d][i]));
+            x *= f;
+            float y;
+            asm volatile("v_accvgpr_write_b32 %0, %1\n\ts_nop 1" : "=a"(y) : "v"(x));
+            o[d][i] = y;
+        }
+}
+
 template <int D, int NW>
 __global__ void __launch_bounds__((64 * NW), (D == 256 ? 1 : 2))
 attn_tile_kernel(AttnArgs a)
@@ -1190,9 +1214,13 @@ attn_tile_kernel(AttnArgs a)
             const float g = __builtin_amdgcn_exp2f(m - now);
             m = now;
             l *= g;
+            if constexpr (D < 256) {
 #pragma unroll
-            for (int d = 0; d < D / 32; d++)
-                o[d] *= g;
+                for (int d = 0; d < D / 32; d++)
+                    o[d] *= g;
+            } else {
+                scale_acc(o, g);
+            }
         }
         const float lift = kAttnLift - m;
         // ---- P^T of 16 tokens, and O^T += V^T P^T of the 16 before

@@ -2235,13 +2235,11 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.seqs = seqs;
     a.pages = pages_per_seq;
     a.page = page_size;
-    if (page_size > 16) {
-        // d = page / 16 in (2^s, 2^(s+1)], mul = ceil(2^(32+s) / d): exact for t / 16 < 2^27
-        const uint64_t d = page_size / 16;
-        while ((2ull << a.page_shift) < d)
-            a.page_shift++;
-        a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
-    }
+    // d = page / 8 in (2^s, 2^(s+1)], mul = ceil(2^(32+s) / d) < 2^32: n * mul >> (32 + s) is n / d for n < 2^31
+    const uint64_t d = page_size / 8;
+    while ((2ull << a.page_shift) < d)
+        a.page_shift++;
+    a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
     a.kv_heads = kv_heads;
     a.group = q_heads / kv_heads;
     a.scale_log2 = scale * 1.44269504089f;
