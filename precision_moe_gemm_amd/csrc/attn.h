@@ -918,6 +918,9 @@ NVFP4_DEV int tile_chunk(int r, int c)
     return r * C + (c ^ (C >= 16 ? r & 15 : ((r >> 1) ^ (r >> 4)) & 7));
 }
 
+// (a kernel's pieces: a call would put the registers that they share in memory)
+#define ATTN_INLINE __attribute__((always_inline))
+
 // f(integral_constant<int, B>), ..., f(integral_constant<int, E - 1>)
 template <int B, int E, class F>
 NVFP4_DEV void for_range(F f)
@@ -933,11 +936,11 @@ NVFP4_DEV float16_t mfma32(half8_t a, half8_t b, float16_t c)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// What a thread of NT holds of a block on its way: kK elements of one token
-// of K, and kV elements of four tokens of V.
-template <int D, int NT>
+// What one of 256 threads holds of a block on its way: kK elements of one
+// token of K, and kV elements of four tokens of V.
+template <int D>
 struct TileRaw {
-    static constexpr int kK = kTileTok * D / NT, kV = kK / 4;
+    static constexpr int kK = kTileTok * D / 256, kV = kK / 4;
     static constexpr int kUnits = kK / 8;  // pieces of decoding of K (8 elements each) and of V (2 of each token)
     uint32_t kc[kK / 8];
     uint32_t ks;
@@ -1009,16 +1012,26 @@ attn_tile_kernel(AttnArgs a)
 {
     constexpr int NT = 64 * NW, ROWS = 32 * NW;
     constexpr int KC = D / 8;  // chunks of a K row
-    typedef TileRaw<D, NT> Raw;
-    __shared__ __attribute__((aligned(16))) u32x4 lk[2][kTileTok * KC];
-    __shared__ __attribute__((aligned(16))) u32x4 lv[2][D * 8];
+    typedef TileRaw<D> Raw;
+    // Eight waves: two on each SIMD, in two groups that take turns.  While one
+    // group multiplies S^T (and decodes), the other weighs P and multiplies
+    // O^T, half a block behind; waves that all waited at one barrier a block
+    // stood in the same phase and hardly overlapped the matrix unit with the
+    // rest.  The first group decodes K and the second V: what either writes is
+    // then read by both a barrier later and no longer by anybody when it is
+    // written again.  Four waves decode both.
+    constexpr bool kTurns = NW == 8;
+    // (separate arrays, picked at compile time, so that the compiler may move
+    // the reads of one buffer past the writes of the other)
+    __shared__ __attribute__((aligned(16))) u32x4 lk0[kTileTok * KC], lk1[kTileTok * KC];
+    __shared__ __attribute__((aligned(16))) u32x4 lv0[D * 8], lv1[D * 8];
     __shared__ __attribute__((aligned(16))) int lok[2][4];  // which 16 tokens lie in a page of the cache
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, e = lane >> 5;
     const int wave = uniform(tid >> 6);
     // ---- the tile: heavy ones first (causal tiles grow towards the end)
     const int h = blockIdx.x % a.kv_heads;
     const int split = blockIdx.y;
-    auto count = [&](int b) {
+    auto count = [&](int b) ATTN_INLINE {
         const AttnSeq s = attn_seq(a, b);
         return AttnCount{(s.nq * a.group + ROWS - 1) / ROWS, 1};
     };
@@ -1080,8 +1093,9 @@ attn_tile_kernel(AttnArgs a)
     const int32_t* table = a.table + f.seq * a.ld_table;
     const int first_page = attn_page(a, lo0), last_page = attn_page(a, hi1 > 0 ? hi1 - 1 : 0);
     const int64_t crow = (int64_t)a.kv_heads * (D / 2), srow = (int64_t)a.kv_heads * (D / 16);
-    const int kt = tid / (D / Raw::kK), kd = tid % (D / Raw::kK) * Raw::kK;
-    const int vt = tid / (D / Raw::kV), vd = tid % (D / Raw::kV) * Raw::kV;
+    const int job = tid & 255;
+    const int kt = job / (D / Raw::kK), kd = job % (D / Raw::kK) * Raw::kK;
+    const int vt = job / (D / Raw::kV), vd = job % (D / Raw::kV) * Raw::kV;
     const uint8_t* const k_codes = a.k_packed + h * (D / 2) + kd / 2;
     const uint8_t* const k_scales = a.k_scales + h * (D / 16) + kd / 16;
     const uint8_t* const v_codes = a.v_packed + h * (D / 2) + vd / 2;
@@ -1090,26 +1104,26 @@ attn_tile_kernel(AttnArgs a)
     int kp = 0, vp = 0;  // the pages of the next block's tokens
     bool bad = false;
     // the entry of the page of token t (past the end: the last page, masked)
-    auto entry = [&](int t) {
+    auto entry = [&](int t) ATTN_INLINE {
         const int i = attn_page(a, t);
         return table[i < last_page ? i : last_page];
     };
-    auto pages = [&](int blk) {
-        kp = entry(blk * kTileTok + kt);
-        vp = entry(blk * kTileTok + 4 * vt);
-    };
+    auto pages_k = [&](int blk) ATTN_INLINE { kp = entry(blk * kTileTok + kt); };
+    auto pages_v = [&](int blk) ATTN_INLINE { vp = entry(blk * kTileTok + 4 * vt); };
     // the first row of token t in the cache; a page that is none of the cache's: page 0
-    auto row_of = [&](int page, int t, bool* ok) {
+    auto row_of = [&](int page, int t, bool* ok) ATTN_INLINE {
         const int i = attn_page(a, t);
         *ok = page >= 0 && page < a.num_pages;
         // (a page with no token that a row sees may hold anything)
         bad |= !*ok && t < hi1 && i >= first_page;
         return (int64_t)(*ok ? page : 0) * a.page + (t - i * a.page);
     };
-    auto load = [&](int blk) {
+    auto load_k = [&](int blk) ATTN_INLINE {
         const int64_t k = row_of(kp, blk * kTileTok + kt, &raw.ok);
         load_bytes<Raw::kK / 2>(k_codes + k * crow, raw.kc);
         load_bytes<(Raw::kK > 16 ? Raw::kK / 16 : 1)>(k_scales + k * srow, &raw.ks);
+    };
+    auto load_v = [&](int blk) ATTN_INLINE {
         bool ok;
         const int64_t v = row_of(vp, blk * kTileTok + 4 * vt, &ok);
 #pragma unroll
@@ -1121,7 +1135,7 @@ attn_tile_kernel(AttnArgs a)
     // V's codes with two tokens side by side: byte i of even / odd: elements 2i / 2i + 1
     uint32_t even[2][Raw::kV > 8 ? Raw::kV / 8 : 1], odd[2][Raw::kV > 8 ? Raw::kV / 8 : 1];
     half2_t vsc[2];
-    auto interleave = [&](int buf) {
+    auto interleave = [&]() ATTN_INLINE {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
 #pragma unroll
@@ -1132,26 +1146,25 @@ attn_tile_kernel(AttnArgs a)
             }
             vsc[i] = scale_pair(raw.vs[2 * i], raw.vs[2 * i + 1]);
         }
-        if (kd == 0 && (kt & 15) == 0)
-            lok[buf][kt >> 4] = raw.ok;
     };
     // tokens 4 vt .. + 4 of the block: 8 bytes at place 8 (vt % 2) + 4 (vt / 2 % 2) of their 16
     const int vchunk = 2 * (vt >> 2) + (vt & 1), vpart = (vt >> 1) & 1;
-    // piece U of decoding the block in raw into buffer buf
-    auto decode = [&](int buf, auto unit) {
-        constexpr int U = decltype(unit)::value;
+    // piece U of decoding the block in raw into buffer B
+    auto decode_k = [&](auto buf, auto unit) ATTN_INLINE {
+        constexpr int B = decltype(buf)::value, U = decltype(unit)::value;
         const uint32_t b = raw.ks >> (8 * (U >> 1));
-        lk[buf][tile_chunk<KC>(kt, kd / 8 + U)] = __builtin_bit_cast(u32x4, decode_row8(raw.kc[U], scale_pair(b, b)));
-        u32x2* dst = (u32x2*)lv[buf] + vpart;
-        constexpr int W = U / 4, I = U % 4;
+        (B ? lk1 : lk0)[tile_chunk<KC>(kt, kd / 8 + U)] =
+            __builtin_bit_cast(u32x4, decode_row8(raw.kc[U], scale_pair(b, b)));
+        if (U == 0 && kd == 0 && (kt & 15) == 0)
+            lok[B][kt >> 4] = raw.ok;
+    };
+    auto decode_v = [&](auto buf, auto unit) ATTN_INLINE {
+        constexpr int B = decltype(buf)::value, U = decltype(unit)::value, W = U / 4, I = U % 4;
+        u32x2* dst = (u32x2*)(B ? lv1 : lv0) + vpart;
         dst[2 * tile_chunk<8>(vd + 2 * U, vchunk)] =
             (u32x2){decode_pair<I>(even[0][W], vsc[0]), decode_pair<I>(even[1][W], vsc[1])};
         dst[2 * tile_chunk<8>(vd + 2 * U + 1, vchunk)] =
             (u32x2){decode_pair<I>(odd[0][W], vsc[0]), decode_pair<I>(odd[1][W], vsc[1])};
-    };
-    auto decode_all = [&](int buf) {
-        interleave(buf);
-        for_range<0, Raw::kUnits>([&](auto u) { decode(buf, u); });
     };
 
     float16_t o[D / 32];
@@ -1161,38 +1174,56 @@ attn_tile_kernel(AttnArgs a)
         for (int i = 0; i < 16; i++)
             o[d][i] = 0.0f;
     float m = kAttnLow, l = 0.0f;
-    if (b0 < b1) {
-        pages(b0);
-        load(b0);
-        pages(b0 + 1);
-        decode_all(0);
-        load(b0 + 1);
-        pages(b0 + 2);
-    }
-    // (past the end the loads go to the last page again and are not used)
-    for (int blk = b0; blk < b1; blk++) {
-        const int buf = (blk - b0) & 1;
-        __syncthreads();  // buffer `buf` is written, and nobody reads the other any more
-        const int t0 = blk * kTileTok;
-        const u32x4 ok = *(const u32x4*)lok[buf];
-        // ---- S^T, and between its products the decoding of the next block
-        interleave(buf ^ 1);
-        float16_t sc[2];
+    float16_t sc[2];
+    u32x4 ok;  // which 16 tokens of the block lie in a page of the cache
+    // S^T of block blk, and between its products the decoding of the next one
+    // (what of it is this wave's) and the requests for the one after.  Past the
+    // end these go to the last page again and are not used.
+    auto multiply = [&](int blk, auto buf, auto has_k, auto has_v) ATTN_INLINE {
+        constexpr int B = decltype(buf)::value, kAhead = 2, N = D / 16;
+        const std::integral_constant<int, 1 - B> other{};
+        ok = *(const u32x4*)lok[B];
+        if constexpr (has_v)
+            interleave();
 #pragma unroll
         for (int p = 0; p < 2; p++)
 #pragma unroll
             for (int i = 0; i < 16; i++)
                 sc[p][i] = 0.0f;
-        for_range<0, D / 16>([&](auto ci) {
-            constexpr int c = decltype(ci)::value, per = D / 16 / Raw::kUnits;  // (kUnits <= D / 16)
+        // (operands are read two product steps ahead)
+        half8_t f[N][2];
+        auto read = [&](auto ci) ATTN_INLINE {
+            constexpr int c = decltype(ci)::value;
 #pragma unroll
             for (int p = 0; p < 2; p++)
-                sc[p] = mfma32(__builtin_bit_cast(half8_t, lk[buf][tile_chunk<KC>(32 * p + col, 2 * c + e)]), q[c], sc[p]);
-            if constexpr (c % per == per - 1)
-                decode(buf ^ 1, std::integral_constant<int, c / per>{});
+                f[c][p] = __builtin_bit_cast(half8_t, (B ? lk1 : lk0)[tile_chunk<KC>(32 * p + col, 2 * c + e)]);
+        };
+        for_range<0, kAhead>(read);
+        for_range<0, N>([&](auto ci) ATTN_INLINE {
+            constexpr int c = decltype(ci)::value, per = N / Raw::kUnits;  // (2)
+            if constexpr (c + kAhead < N)
+                read(std::integral_constant<int, c + kAhead>{});
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+                sc[p] = mfma32(f[c][p], q[c], sc[p]);
+            if constexpr (has_k && c % per == 0)
+                decode_k(other, std::integral_constant<int, c / per>{});
+            if constexpr (has_v && c % per == per - 1)
+                decode_v(other, std::integral_constant<int, c / per>{});
         });
-        load(blk + 2);
-        pages(blk + 3);
+        if constexpr (has_k) {
+            load_k(blk + 2);
+            pages_k(blk + 3);
+        }
+        if constexpr (has_v) {
+            load_v(blk + 2);
+            pages_v(blk + 3);
+        }
+    };
+    // P^T of block blk, and O^T += V^T P^T
+    auto accumulate = [&](int blk, auto buf) ATTN_INLINE {
+        constexpr int B = decltype(buf)::value, N = D / 32, kAhead = 4;
+        const int t0 = blk * kTileTok;
         if (!(t0 >= lo1 && t0 + kTileTok <= hi0 && (ok.x & ok.y & ok.z & ok.w) != 0)) {
 #pragma unroll
             for (int p = 0; p < 2; p++)
@@ -1223,9 +1254,8 @@ attn_tile_kernel(AttnArgs a)
             }
         }
         const float lift = kAttnLift - m;
-        // ---- P^T of 16 tokens, and O^T += V^T P^T of the 16 before
         half8_t pt[4];
-        auto weigh = [&](int k) {
+        auto weigh = [&](int k) ATTN_INLINE {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -1235,14 +1265,88 @@ attn_tile_kernel(AttnArgs a)
             for (int i = 0; i < 8; i++)
                 pt[k][i] = (_Float16)x[i];
         };
+        // each 16 tokens are weighed between the products of the 16 before;
+        // operands are read four products ahead
+        half8_t f[4 * N];
+        auto read = [&](auto xi) ATTN_INLINE {
+            constexpr int x = decltype(xi)::value;
+            f[x] = __builtin_bit_cast(half8_t, (B ? lv1 : lv0)[tile_chunk<8>(32 * (x % N) + col, 2 * (x / N) + e)]);
+        };
+        for_range<0, kAhead>(read);
         weigh(0);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            if (k < 3)
+        for_range<0, 4 * N>([&](auto xi) ATTN_INLINE {
+            constexpr int x = decltype(xi)::value, k = x / N, d = x % N;
+            if constexpr (d == 0 && k < 3)
                 weigh(k + 1);
-#pragma unroll
-            for (int d = 0; d < D / 32; d++)
-                o[d] = mfma32(__builtin_bit_cast(half8_t, lv[buf][tile_chunk<8>(32 * d + col, 2 * k + e)]), pt[k], o[d]);
+            if constexpr (x + kAhead < 4 * N)
+                read(std::integral_constant<int, x + kAhead>{});
+            o[d] = mfma32(f[x], pt[k], o[d]);
+        });
+    };
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
+    auto prepare = [&](auto has_k, auto has_v) ATTN_INLINE {
+        if constexpr (has_k) {
+            pages_k(b0);
+            load_k(b0);
+            pages_k(b0 + 1);
+            for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE { decode_k(zero, u); });
+            load_k(b0 + 1);
+            pages_k(b0 + 2);
+        }
+        if constexpr (has_v) {
+            pages_v(b0);
+            load_v(b0);
+            pages_v(b0 + 1);
+            interleave();
+            for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE { decode_v(zero, u); });
+            load_v(b0 + 1);
+            pages_v(b0 + 2);
+        }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (b0 < b1) {
+        if constexpr (!kTurns) {
+            prepare(yes, yes);
+            auto turn = [&](int blk, auto buf) ATTN_INLINE {
+                lds_barrier();  // the block is written, and nobody reads the other buffer any more
+                multiply(blk, buf, yes, yes);
+                accumulate(blk, buf);
+            };
+            for (int blk = b0; blk < b1; blk += 2) {
+                turn(blk, zero);
+                if (blk + 1 < b1)
+                    turn(blk + 1, one);
+            }
+        } else if (wave < NW / 2) {
+            prepare(yes, no);
+            lds_barrier();
+            auto turn = [&](int blk, auto buf) ATTN_INLINE {
+                multiply(blk, buf, yes, no);
+                lds_barrier();
+                accumulate(blk, buf);
+                lds_barrier();
+            };
+            for (int blk = b0; blk < b1; blk += 2) {
+                turn(blk, zero);
+                if (blk + 1 < b1)
+                    turn(blk + 1, one);
+            }
+        } else {
+            prepare(no, yes);
+            lds_barrier();
+            auto turn = [&](int blk, auto buf) ATTN_INLINE {
+                lds_barrier();  // half a block behind
+                multiply(blk, buf, no, yes);
+                lds_barrier();
+                accumulate(blk, buf);
+            };
+            for (int blk = b0; blk < b1; blk += 2) {
+                turn(blk, zero);
+                if (blk + 1 < b1)
+                    turn(blk + 1, one);
+            }
         }
     }
     if (bad)
