@@ -1092,9 +1092,10 @@ attn_tile_kernel(AttnArgs a)
     // and of V (tokens 4 vt .. + 4, elements vd .. + kV)
     const int32_t* table = a.table + f.seq * a.ld_table;
     const int first_page = attn_page(a, lo0), last_page = attn_page(a, hi1 > 0 ? hi1 - 1 : 0);
-    const int64_t crow = (int64_t)a.kv_heads * (D / 2), srow = (int64_t)a.kv_heads * (D / 16);
+    const uint32_t crow = a.kv_heads * (D / 2), srow = a.kv_heads * (D / 16);
     const int job = tid & 255;
-    const int kt = job / (D / Raw::kK), kd = job % (D / Raw::kK) * Raw::kK;
+    // (D = 256: K elements kd .. + 32 and 128 + kd .. + 32, whose places in shared memory spread over the banks)
+    const int kt = job / (D / Raw::kK), kd = job % (D / Raw::kK) * (D < 256 ? Raw::kK : 32);
     const int vt = job / (D / Raw::kV), vd = job % (D / Raw::kV) * Raw::kV;
     const uint8_t* const k_codes = a.k_packed + h * (D / 2) + kd / 2;
     const uint8_t* const k_scales = a.k_scales + h * (D / 16) + kd / 16;
@@ -1116,16 +1117,25 @@ attn_tile_kernel(AttnArgs a)
         *ok = page >= 0 && page < a.num_pages;
         // (a page with no token that a row sees may hold anything)
         bad |= !*ok && t < hi1 && i >= first_page;
-        return (int64_t)(*ok ? page : 0) * a.page + (t - i * a.page);
+        return (uint32_t)(*ok ? page : 0) * (uint32_t)a.page + (uint32_t)(t - i * a.page);
     };
     auto load_k = [&](int blk) ATTN_INLINE {
-        const int64_t k = row_of(kp, blk * kTileTok + kt, &raw.ok);
-        load_bytes<Raw::kK / 2>(k_codes + k * crow, raw.kc);
-        load_bytes<(Raw::kK > 16 ? Raw::kK / 16 : 1)>(k_scales + k * srow, &raw.ks);
+        const uint64_t k = row_of(kp, blk * kTileTok + kt, &raw.ok);
+        if constexpr (D < 256) {
+            load_bytes<Raw::kK / 2>(k_codes + k * crow, raw.kc);
+            load_bytes<(Raw::kK > 16 ? Raw::kK / 16 : 1)>(k_scales + k * srow, &raw.ks);
+        } else {
+            uint32_t hi;
+            load_bytes<16>(k_codes + k * crow, raw.kc);
+            load_bytes<16>(k_codes + k * crow + 64, raw.kc + 4);
+            load_bytes<2>(k_scales + k * srow, &raw.ks);
+            load_bytes<2>(k_scales + k * srow + 8, &hi);
+            raw.ks |= hi << 16;
+        }
     };
     auto load_v = [&](int blk) ATTN_INLINE {
         bool ok;
-        const int64_t v = row_of(vp, blk * kTileTok + 4 * vt, &ok);
+        const uint64_t v = row_of(vp, blk * kTileTok + 4 * vt, &ok);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             load_bytes<Raw::kV / 2>(v_codes + (v + i) * crow, raw.vc[i]);
@@ -1153,7 +1163,7 @@ attn_tile_kernel(AttnArgs a)
     auto decode_k = [&](auto buf, auto unit) ATTN_INLINE {
         constexpr int B = decltype(buf)::value, U = decltype(unit)::value;
         const uint32_t b = raw.ks >> (8 * (U >> 1));
-        (B ? lk1 : lk0)[tile_chunk<KC>(kt, kd / 8 + U)] =
+        (B ? lk1 : lk0)[tile_chunk<KC>(kt, kd / 8 + (D < 256 ? U : U % 4 + U / 4 * 16))] =
             __builtin_bit_cast(u32x4, decode_row8(raw.kc[U], scale_pair(b, b)));
         if (U == 0 && kd == 0 && (kt & 15) == 0)
             lok[B][kt >> 4] = raw.ok;
@@ -1181,6 +1191,9 @@ attn_tile_kernel(AttnArgs a)
     // end these go to the last page again and are not used.
     auto multiply = [&](int blk, auto buf, auto has_k, auto has_v) ATTN_INLINE {
         constexpr int B = decltype(buf)::value, kAhead = 2, N = D / 16;
+        // the group that feeds the matrix unit goes first (measured 4% at D = 128; the other way round 1%)
+        if constexpr (kTurns)
+            __builtin_amdgcn_s_setprio(1);
         const std::integral_constant<int, 1 - B> other{};
         ok = *(const u32x4*)lok[B];
         if constexpr (has_v)
@@ -1223,6 +1236,8 @@ attn_tile_kernel(AttnArgs a)
     // P^T of block blk, and O^T += V^T P^T
     auto accumulate = [&](int blk, auto buf) ATTN_INLINE {
         constexpr int B = decltype(buf)::value, N = D / 32, kAhead = 4;
+        if constexpr (kTurns)
+            __builtin_amdgcn_s_setprio(0);
         const int t0 = blk * kTileTok;
         if (!(t0 >= lo1 && t0 + kTileTok <= hi0 && (ok.x & ok.y & ok.z & ok.w) != 0)) {
 #pragma unroll

@@ -2204,7 +2204,7 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     if ((D != 64 && D != 128 && D != 256) || page_size % 16 != 0)
         return NVFP4_ERR_UNSUPPORTED;
     const int64_t num_pages = k_cache->rows / kv_heads / page_size;
-    if ((int64_t)pages_per_seq * page_size > 0x7FFFFF00 || n * q_heads > 0x7FFFFF00 || kv_heads > 4 * 65535)
+    if (k_cache->rows / kv_heads > 0x7FFFFFFF || (int64_t)pages_per_seq * page_size > 0x7FFFFF00 || n * q_heads > 0x7FFFFF00 || kv_heads > 4 * 65535)
         return NVFP4_ERR_UNSUPPORTED;
     if (ld_q < q_heads * D || ld_q % 8 != 0 || ld_out < q_heads * D || ld_out % 8 != 0 ||
         (pages_per_seq > 0 && num_pages < 1))
