@@ -46,11 +46,13 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device=None):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # (the handle alone: building torch's stream object takes longer than a launch)
+    index = None if device is None else torch.device(device).index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _need_cuda(*ts):
@@ -473,9 +475,12 @@ def nvfp4_kv_dequant(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int, tok
     return ko, vo
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """Launches go to the operands' device: make it current if it is not."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _operand(t, what, dtype, dim, device):

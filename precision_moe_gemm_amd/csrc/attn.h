@@ -64,6 +64,7 @@ struct AttnArgs {
     float* lse;              // [n, heads] or null
     int head_lanes;          // KV heads a workgroup holds side by side (1, 2 or 4)
     int workers;             // shares that the tokens are cut into (at most)
+    int whole;               // a workgroup takes a whole tile of rows instead of a share
     struct AttnTile* tiles;  // tiles of rows, as the joining launch needs them
     float* partial;          // what shares leave of tiles that they hold a part of
 };
@@ -735,10 +736,14 @@ attn_rows_kernel(AttnArgs a)
     const int blocks = a.kv_heads / hl;
     const int hb = blockIdx.x / 8 % blocks, w = blockIdx.x / (8 * blocks) * 8 + blockIdx.x % 8;
     const int h = hb * hl + wave % hl, tl = wave / hl;
-    auto count = [&](int b) { return attn_count<D, NT>(a, attn_seq(a, b)); };
+    auto count = [&](int b) {
+        AttnCount c = attn_count<D, NT>(a, attn_seq(a, b));
+        c.units = a.whole ? 1 : c.units;  // whole tiles: w counts tiles
+        return c;
+    };
     const AttnScan scan = attn_scan(a.seqs, count);
-    const int64_t total = scan.units, shares = attn_shares(a, scan.units);
-    if (w == 0 && hb == 0 && threadIdx.x == 0)
+    const int64_t total = scan.units, shares = a.whole ? scan.units : attn_shares(a, scan.units);
+    if (!a.whole && w == 0 && hb == 0 && threadIdx.x == 0)
         a.tiles[0].parts = scan.tiles;
     if (w >= shares)
         return;
@@ -747,7 +752,9 @@ attn_rows_kernel(AttnArgs a)
     AttnFound f = attn_find(scan, a.seqs, u, count);
     while (u < u1) {
         const AttnSeq s = attn_seq_uniform(a, f.seq);
-        const AttnCount c = attn_count<D, NT>(a, s);
+        AttnCount c = attn_count<D, NT>(a, s);
+        const int units = c.units;
+        c.units = a.whole ? 1 : c.units;
         if (f.at >= c.tiles * c.units) {
             f.before.tiles += c.tiles;
             f.before.units += c.tiles * c.units;
@@ -756,10 +763,10 @@ attn_rows_kernel(AttnArgs a)
             continue;
         }
         const int tile = f.at / c.units, first = f.at - tile * c.units;
-        const int n = c.units - first < u1 - u ? c.units - first : u1 - u;
+        const int n = a.whole ? units : (units - first < u1 - u ? units - first : u1 - u);
         const int row0 = tile * 16 * NT;
-        if (first == 0 && hb == 0 && threadIdx.x == 0) {
-            const int64_t end = u + c.units;  // the share of the tile's last unit
+        if (!a.whole && first == 0 && hb == 0 && threadIdx.x == 0) {
+            const int64_t end = u + units;  // the share of the tile's last unit
             a.tiles[1 + f.before.tiles + tile] = AttnTile{w, (int)((end * shares - 1) / total) - w + 1, s.q0, s.nq, row0};
         }
         int any, none, lo0, hi0, lo1, hi1;  // tokens of the sequence's, the tile's first and last row
@@ -783,7 +790,7 @@ attn_rows_kernel(AttnArgs a)
             __syncthreads();
         }
         if (tl == 0) {
-            if (n == c.units) {
+            if (n == units) {
                 attn_finish<D, NT>(a, x, s, h, row0);
             } else {
                 const int slot = first == 0;
@@ -803,8 +810,8 @@ attn_rows_kernel(AttnArgs a)
                 }
             }
         }
-        u += n;
-        f.at += n;
+        u += a.whole ? 1 : n;
+        f.at += a.whole ? 1 : n;
     }
 }
 

@@ -251,13 +251,23 @@ size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64
     return attention_tiles_bytes(n, q_heads / kv_heads, seqs) + align256(part);
 }
 
+constexpr int64_t kWholeTiles = 256, kWholeTokens = 1024;
 template <int D, int NT>
-nvfp4_status launch_attention_rows(const AttnArgs& a, hipStream_t st)
+nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
 {
     const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, 16 * NT);
     // (units are counted in 31 bits)
     if ((double)tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) > 2147483647.0 || a.kv_heads > 65535)
         return NVFP4_ERR_UNSUPPORTED;
+    // Few short sequences: a workgroup per tile and KV head, its waves side by
+    // side over the tokens, and no second launch.
+    if (tiles * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens) {
+        a.whole = 1;
+        a.head_lanes = 1;
+        attn_rows_kernel<D, NT>
+            <<<(unsigned)(ceil_div(tiles, 8) * 8 * a.kv_heads), 64 * attn_waves<D, NT>(), 0, st>>>(a);
+        return launch_status();
+    }
     const int blocks = a.kv_heads / a.head_lanes;
     attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), 64 * attn_waves<D, NT>(), 0, st>>>(a);
     nvfp4_status s = launch_status();
