@@ -313,12 +313,25 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
         return launch_attention_tiles<D, 8>(a, st);
 }
 
-// RMS norm: 1024-thread workgroups, up to 8 chunks of 8 elements per thread.
+// RMS norm: a workgroup per row (up to 16 chunks of 8 elements per thread),
+// rows of up to 256 elements several to a wave.
 constexpr int64_t kNormMaxCols = 65536;
+template <int L>
+void launch_add_rmsnorm_narrow(const NormArgs& a, hipStream_t st)
+{
+    add_rmsnorm_narrow_kernel<L><<<(unsigned)std::min<int64_t>(ceil_div(a.rows, 256 / L), 1 << 20), 256, 0, st>>>(a);
+}
+
 void launch_add_rmsnorm(const NormArgs& a, hipStream_t st)
 {
+    if (a.chunks <= 8)
+        return launch_add_rmsnorm_narrow<8>(a, st);
+    if (a.chunks <= 16)
+        return launch_add_rmsnorm_narrow<16>(a, st);
+    if (a.chunks <= 32)
+        return launch_add_rmsnorm_narrow<32>(a, st);
     const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 1 << 20);
-    const int threads = (int)std::min<int64_t>(1024, ceil_div(a.chunks, 64) * 64);
+    const int threads = (int)std::min<int64_t>(kNormThreads, ceil_div(a.chunks, 64) * 64);
     const int64_t per = ceil_div(a.chunks, threads);
     if (per <= 1)
         add_rmsnorm_kernel<1><<<grid, threads, 0, st>>>(a);
@@ -326,8 +339,10 @@ void launch_add_rmsnorm(const NormArgs& a, hipStream_t st)
         add_rmsnorm_kernel<2><<<grid, threads, 0, st>>>(a);
     else if (per <= 4)
         add_rmsnorm_kernel<4><<<grid, threads, 0, st>>>(a);
-    else
+    else if (per <= 8)
         add_rmsnorm_kernel<8><<<grid, threads, 0, st>>>(a);
+    else
+        add_rmsnorm_kernel<16><<<grid, threads, 0, st>>>(a);
 }
 
 // ---------------------------------------------------------------- GEMM
