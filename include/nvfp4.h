@@ -553,10 +553,15 @@ nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, 
  * Products are exact and summed in fp32 (q is held in f16 relative to its
  * row's largest element, p in f16); results do not depend on anything but the
  * arguments.  An entry that is not a page of the cache, a kv_lens[b] outside
- * [0, pages_per_seq * page_size] or a cu_q that decreases or passes n raises
- * the sticky NVFP4_ERR_RANGE: such a page's tokens are skipped, such a length
- * is cut.  D is 64, 128 or 256 and page_size % 16 == 0 on this build (else
- * NVFP4_ERR_UNSUPPORTED); scale finite and positive.
+ * [0, pages_per_seq * page_size] or a cu_q that decreases or leaves [0, n]
+ * raises the sticky NVFP4_ERR_RANGE: such a page's tokens are skipped, such a
+ * length or offset is cut, and a cu_q that decreases writes nothing at all.
+ * A row of q with a NaN or infinity spoils its own output alone.  Calls that
+ * may overlap in time (other streams, two captured graphs) need a workspace
+ * each.  With the data checks on, q and the globals are checked, not the
+ * caches' scales: unwritten pages may hold anything.  D is 64, 128 or 256 and
+ * page_size % 16 == 0 on this build, and a cache has fewer than 2^31 tokens
+ * (else NVFP4_ERR_UNSUPPORTED); scale finite and positive.
  */
 nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads,
                                 const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,

@@ -51,7 +51,12 @@ def _ptr(t):
 
 def _stream(device=None):
     # (the handle alone: building torch's stream object takes longer than a launch)
-    index = None if device is None else torch.device(device).index
+    index = None
+    if device is not None:
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("libnvfp4 operates on device tensors")
+        index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
@@ -575,6 +580,8 @@ def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tens
     seqs, pages = block_table.shape
     if kv_lens.numel() != seqs:
         raise ValueError("kv_lens: one per row of block_table")
+    if seqs > 1 and block_table.stride(0) < pages:
+        raise ValueError("block_table: rows must not overlap")
     if cu_q is not None:
         _operand(cu_q, "cu_q", torch.int32, 1, device)
         if cu_q.numel() != seqs + 1:
@@ -594,14 +601,16 @@ def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tens
         if lse.shape != (n, q_heads) or not lse.is_contiguous():
             raise ValueError("lse: a contiguous [n, q_heads] tensor is expected")
     lib = _lib.load()
-    if ws is None:
+    if ws is not None:
+        _operand(ws, "ws", torch.uint8, 1, device)
+    else:
         need = lib.nvfp4_workspace_size(_lib.OP_KV_ATTENTION, n, q_heads, heads, D, seqs)
         ws = _workspace(need, device) if need else None
     kc, vc = k_cache.c(), v_cache.c()
     with _on(device):
         st = lib.nvfp4_kv_attention(
             _ptr(q), ld_q, n, q_heads, ctypes.byref(kc), ctypes.byref(vc), heads, _ptr(block_table),
-            max(block_table.stride(0), pages), pages, page_size, _ptr(kv_lens), _ptr(cu_q), seqs, max_q,
+            block_table.stride(0) if seqs > 1 else pages, pages, page_size, _ptr(kv_lens), _ptr(cu_q), seqs, max_q,
             D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), ld_out, _ptr(lse), _ptr(ws),
             0 if ws is None else ws.numel(), _stream(device))
     _check(st, "nvfp4_kv_attention")

@@ -14,8 +14,8 @@
 // (K's to the scores, V's to the output).  q (bf16) is scaled per row by a
 // power of two to a largest magnitude in [1, 2) and held in f16: exact for
 // every element down to 2^-16 of the row's largest, and off by at most 2^-25
-// of that below.  p is rounded to f16 for the second product (half a step is
-// 2^-12 of it), l sums the unrounded p.
+// of that below.  p is rounded to f16 for the second product (off by at
+// most 2^-11 of it), l sums the unrounded p.
 //
 // Both products are written transposed, S^T = K Q^T and O^T = V^T P^T, with
 // v_mfma_f32_16x16x32_f16 (A: row l % 16, B: column l % 16, both elements
@@ -80,9 +80,10 @@ constexpr float kAttnLazy = 8.0f;        // growth of the maximum (log 2) that i
 constexpr float kAttnLift = 7.0f;        // p is held times 2^7, at most 2^15 (f16 holds 65504)
 
 // One sequence as the kernels see it: bad lengths are cut to what exists and
-// raise NVFP4_ERR_RANGE.
+// raise NVFP4_ERR_RANGE.  down: its end lies before its start.
 struct AttnSeq {
     int q0, nq, kv;
+    bool down;
 };
 
 // The page of token t >= 0 of a sequence.
@@ -106,9 +107,11 @@ NVFP4_DEV AttnSeq attn_seq(const AttnArgs& a, int b)
         const int e = hi < s.q0 ? s.q0 : (hi > n ? n : hi);
         s.nq = e - s.q0;
         bad = s.q0 != lo || e != hi;
+        s.down = hi < lo;
     } else {
         s.q0 = b;
         s.nq = 1;
+        s.down = false;
     }
     const int kv = a.kv_lens[b];
     const int64_t most = (int64_t)a.pages * a.page;
@@ -125,17 +128,18 @@ NVFP4_DEV void attn_limits(const AttnArgs& a, const AttnSeq& s, int i, int* star
     if (a.causal) {
         const int pos = s.kv - s.nq + i;  // its own position
         e = pos + 1 < s.kv ? pos + 1 : s.kv;
-        if (a.window > 0)
+        // (pos may be far below zero: pos - window could wrap)
+        if (a.window > 0 && pos >= a.window)
             b = pos - a.window + 1;
     }
     *end = e < 0 ? 0 : e;
-    *start = b < 0 ? 0 : b;
+    *start = b;
 }
 
 NVFP4_DEV AttnSeq attn_seq_uniform(const AttnArgs& a, int b)
 {
     const AttnSeq s = attn_seq(a, b);
-    return AttnSeq{uniform(s.q0), uniform(s.nq), uniform(s.kv)};
+    return AttnSeq{uniform(s.q0), uniform(s.nq), uniform(s.kv), s.down};
 }
 
 // Work of a row kernel is counted in units: sequence b has `tiles` tiles of
@@ -144,10 +148,13 @@ NVFP4_DEV AttnSeq attn_seq_uniform(const AttnArgs& a, int b)
 // units could pass 31 bits.
 struct AttnCount {
     int tiles, units;
+    bool down;
 };
 
 // Every wave scans all sequences by itself: lane l sums the run of
-// sequences [l per, + per).
+// sequences [l per, + per).  Offsets that go down anywhere (rows would then
+// belong to several sequences, and their number would have no bound) leave
+// no work at all.
 struct AttnScan {
     AttnCount before;  // tiles and units before this lane's run
     int mine;          // units of the run
@@ -161,8 +168,10 @@ NVFP4_DEV AttnScan attn_scan(int seqs, Count count)
     const int per = (seqs + 63) >> 6;
     const int b0 = lane * per, b1 = b0 + per < seqs ? b0 + per : seqs;
     int tiles = 0, units = 0;
+    bool down = false;
     for (int b = b0; b < b1; b++) {
         const AttnCount c = count(b);
+        down |= c.down;
         tiles += c.tiles;
         units += c.tiles * c.units;
     }
@@ -177,8 +186,9 @@ NVFP4_DEV AttnScan attn_scan(int seqs, Count count)
     s.before.tiles = ut - tiles;
     s.before.units = uu - units;
     s.mine = units;
-    s.tiles = __builtin_amdgcn_readlane(ut, 63);
-    s.units = __builtin_amdgcn_readlane(uu, 63);
+    const bool none = __any(down);
+    s.tiles = none ? 0 : __builtin_amdgcn_readlane(ut, 63);
+    s.units = none ? 0 : __builtin_amdgcn_readlane(uu, 63);
     return s;
 }
 
@@ -658,7 +668,7 @@ NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT>& w, const At
             continue;
         const int head = h * a.group + hh;
         const int64_t token = s.q0 + i;
-        const float f = w.l[t] > 0.0f ? vg / w.l[t] : 0.0f;  // a row that sees nothing: zeros
+        const float f = w.l[t] != 0.0f ? vg / w.l[t] : 0.0f;  // a row that sees nothing: zeros
         uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + 4 * lane_g() * (D / 16);
 #pragma unroll
         for (int k = 0; k < 4; k++)
@@ -669,8 +679,8 @@ NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT>& w, const At
                             pack_bf16x2(w.o[t][dd + 2][k] * f, w.o[t][dd + 3][k] * f)};
         if (a.lse && lane_g() == 0)
             a.lse[token * (a.kv_heads * a.group) + head] =
-                w.l[t] > 0.0f ? (w.m[t] - kAttnLift + __builtin_amdgcn_logf(w.l[t])) * 0.69314718056f
-                              : -__builtin_inff();
+                w.l[t] != 0.0f ? (w.m[t] - kAttnLift + __builtin_amdgcn_logf(w.l[t])) * 0.69314718056f
+                               : -__builtin_inff();
     }
 }
 
@@ -702,6 +712,7 @@ NVFP4_DEV AttnCount attn_count(const AttnArgs& a, const AttnSeq& s)
     AttnCount c;
     c.tiles = (s.nq * a.group + 16 * NT - 1) / (16 * NT);
     c.units = hi1 > t0 ? (hi1 - t0 + kAttnStep - 1) / kAttnStep : 1;
+    c.down = s.down;
     return c;
 }
 
@@ -888,12 +899,12 @@ attn_combine_kernel(AttnArgs a, int pieces)
             }
             if (pw != 0 || !in)
                 continue;
-            const float scale = l > 0.0f ? vg / l : 0.0f;
+            const float scale = l != 0.0f ? vg / l : 0.0f;
             *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
                 (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
             if (a.lse && c == 0 && g == 0)
                 a.lse[token * (a.kv_heads * a.group) + head] =
-                    l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+                    l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
         }
     }
 }
@@ -1040,7 +1051,7 @@ attn_tile_kernel(AttnArgs a)
     const int split = blockIdx.y;
     auto count = [&](int b) ATTN_INLINE {
         const AttnSeq s = attn_seq(a, b);
-        return AttnCount{(s.nq * a.group + ROWS - 1) / ROWS, 1};
+        return AttnCount{(s.nq * a.group + ROWS - 1) / ROWS, 1, s.down};
     };
     const AttnScan scan = attn_scan(a.seqs, count);
     const int slot = blockIdx.x / a.kv_heads;
@@ -1397,7 +1408,7 @@ attn_tile_kernel(AttnArgs a)
     }
     if (!in)
         return;
-    const float g = l > 0.0f ? *a.v_global / l : 0.0f;
+    const float g = l != 0.0f ? *a.v_global / l : 0.0f;
     uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + 4 * e;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
@@ -1407,7 +1418,7 @@ attn_tile_kernel(AttnArgs a)
                                                       pack_bf16x2(o[d][4 * i + 2] * g, o[d][4 * i + 3] * g)};
     if (a.lse && e == 0)
         a.lse[token * (a.kv_heads * a.group) + head] =
-            l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+            l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
 }
 
 // Joins the splits of a tile of ROWS rows (blockIdx.x) and KV head
@@ -1445,7 +1456,7 @@ attn_tile_combine_kernel(AttnArgs a)
             m = now;
         }
         const int64_t token = tile.q0 + i;
-        const float scale = l > 0.0f ? vg / l : 0.0f;
+        const float scale = l != 0.0f ? vg / l : 0.0f;
         uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + lane * V;
         if constexpr (V == 1)
             *dst = f32_to_bf16(o[0] * scale);
@@ -1455,7 +1466,7 @@ attn_tile_combine_kernel(AttnArgs a)
                 *(uint32_t*)(dst + j) = pack_bf16x2(o[j] * scale, o[j + 1] * scale);
         if (a.lse && lane == 0)
             a.lse[token * (a.kv_heads * a.group) + head] =
-                l > 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+                l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
     }
 }
 

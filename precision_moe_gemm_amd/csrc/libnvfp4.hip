@@ -251,14 +251,19 @@ size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64
     return attention_tiles_bytes(n, q_heads / kv_heads, seqs) + align256(part);
 }
 
+// The row kernel counts its units in 31 bits, and its joining launch takes
+// 1024 threads per tile; what does not fit goes to the tile kernel.
+bool attention_rows_fit(const AttnArgs& a, int rows)
+{
+    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, rows);
+    return tiles <= 0x3FFFFF && tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) <= 0x7FFFFFFF;
+}
+
 constexpr int64_t kWholeTiles = 256, kWholeTokens = 1024;
 template <int D, int NT>
 nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
 {
     const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, 16 * NT);
-    // (units are counted in 31 bits)
-    if ((double)tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) > 2147483647.0 || a.kv_heads > 65535)
-        return NVFP4_ERR_UNSUPPORTED;
     // Few short sequences: a workgroup per tile and KV head, its waves side by
     // side over the tokens, and no second launch.
     if (tiles * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens) {
@@ -286,7 +291,7 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
 {
     constexpr int ROWS = 32 * NW;
     const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, ROWS);
-    if (tiles * a.kv_heads > 0x7FFFFFFF || a.kv_heads > 65535)
+    if (tiles * a.kv_heads * 64 * NW > 0xFFFFFFFF)  // threads of one dimension of a launch
         return NVFP4_ERR_UNSUPPORTED;
     const int64_t splits = std::min(attention_tile_splits(tiles, a.kv_heads),
                                     std::max<int64_t>(1, (int64_t)a.pages * a.page / (4 * kTileTok)));
@@ -303,9 +308,9 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
 {
     a.head_lanes = attention_head_lanes(a.kv_heads);
     a.workers = attention_workers(a.kv_heads, a.head_lanes);
-    if (max_q * a.group <= 16)
+    if (max_q * a.group <= 16 && attention_rows_fit(a, 16))
         return launch_attention_rows<D, 1>(a, st);
-    if (max_q * a.group <= 32)
+    if (max_q * a.group <= 32 && attention_rows_fit(a, 32))
         return launch_attention_rows<D, 2>(a, st);
     if (D == 256 || max_q * a.group <= 128)
         return launch_attention_tiles<D, 4>(a, st);
@@ -2229,7 +2234,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     if ((D != 64 && D != 128 && D != 256) || page_size % 16 != 0)
         return NVFP4_ERR_UNSUPPORTED;
     const int64_t num_pages = k_cache->rows / kv_heads / page_size;
-    if (k_cache->rows / kv_heads > 0x7FFFFFFF || (int64_t)pages_per_seq * page_size > 0x7FFFFF00 || n * q_heads > 0x7FFFFF00 || kv_heads > 4 * 65535)
+    if (k_cache->rows / kv_heads > 0x7FFFFFFF || (int64_t)pages_per_seq * page_size > 0x7FFFFF00 || n > 0x7FFFFF00 ||
+        n * q_heads > 0x7FFFFF00 || kv_heads > 65535)
         return NVFP4_ERR_UNSUPPORTED;
     if (ld_q < q_heads * D || ld_q % 8 != 0 || ld_out < q_heads * D || ld_out % 8 != 0 ||
         (pages_per_seq > 0 && num_pages < 1))
@@ -2281,8 +2287,11 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
                      : D == 128 ? launch_attention<128>(a, max_q, S(stream))
                                 : launch_attention<256>(a, max_q, S(stream));
     if (s == NVFP4_OK && checks_on()) {
+        // (pages that no sequence holds may be unwritten: no check of the scales)
         check_bf16(q, n, q_heads * D, ld_q, S(stream));
-        s = check_tensors_data({k_cache, v_cache}, S(stream));
+        check_globals(k_cache->global, 1, S(stream));
+        check_globals(v_cache->global, 1, S(stream));
+        s = launch_status();
     }
     return s;
 }

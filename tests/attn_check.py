@@ -23,8 +23,9 @@ def attention(q, k_cache, v_cache, heads, table, kv_lens, page, cu_q=None, scale
     of them, in any order) and two more roundings: off by at most (D + 4) steps of sum |q k| scale = S;
     q's elements below 2^-16 of their row's largest are off by 2^-25 of that largest: one more step of
     D max |q| max |k| scale, taken as S2.  exp of it is off by that, relatively, in numerator and
-    denominator both.  p is rounded to f16 (2^-12; 2^-32 absolute where it is subnormal there, of a
-    maximum of 1), the sums over kv tokens run in fp32 (at most kv / 8 + 64 additions in a row, the
+    denominator both.  p is rounded to f16 (2^-11: a value in [1, 2) is a multiple of 2^-10 there, so
+    off by at most 2^-11, and by as much relatively at 1; 2^-32 absolute where it is subnormal there,
+    of a maximum of 1), the sums over kv tokens run in fp32 (at most kv / 8 + 64 additions in a row, the
     matrix instruction's eight at a time, doubled for the rescalings), and the result is rounded to bf16."""
     n, qh, D = q.shape
     g = qh // heads
@@ -67,7 +68,7 @@ def attention(q, k_cache, v_cache, heads, table, kv_lens, page, cu_q=None, scale
                 out[cu[b] + i, rows], lse[cu[b] + i, rows] = o, z
                 rel = (D + 4) * STEP * S + STEP * S2
                 run = 2 * (len(t) / 8 + 64) * STEP
-                tol[cu[b] + i, rows] = (o.abs() * 2.0 ** -8 + (p @ vv.abs()) * (2.0 ** -12 + 2 * rel + run)[:, None]
+                tol[cu[b] + i, rows] = (o.abs() * 2.0 ** -8 + (p @ vv.abs()) * (2.0 ** -11 + 2 * rel + run)[:, None]
                                         + 2.0 ** -31 * vv.abs().sum(0) * p.amax(1)[:, None])
                 ltol[cu[b] + i, rows] = rel + run + 4 * STEP * (z.abs() + sc.abs().amax(1))
     return out, lse, tol, ltol

@@ -125,6 +125,43 @@ def test_attention_refusals(lib):
     assert attend(lib, cu=P(66)) == L.INVALID_ARG
 
 
+def test_attention_workspace_and_limits(lib):
+    from precision_moe_gemm_amd import _lib as L
+    need = lib.nvfp4_workspace_size(L.OP_KV_ATTENTION, 3, 4, 2, 128, 3)
+    assert need > 0 and need % 256 == 0
+    assert attend(lib, ws_bytes=need - 1) == L.WORKSPACE
+    assert attend(lib, ws_bytes=0) == L.WORKSPACE
+    assert attend(lib, ws=P((1 << 20) + 128)) == L.INVALID_ARG
+    c = cache()
+    a = dict(ATTEND)
+    args = [a["q"], a["ld_q"], 3, 4, ctypes.byref(c), ctypes.byref(c), 2, a["table"], 2, 2, 16, a["lens"], None, 3, 1,
+            0.1, 1, 0, a["out"], a["ld_out"], None, None, need, None]
+    assert lib.nvfp4_kv_attention(*args) == L.INVALID_ARG       # no workspace
+    for n in (0, -1):
+        assert lib.nvfp4_workspace_size(L.OP_KV_ATTENTION, n, 4, 2, 128, 3) == 0
+        assert lib.nvfp4_workspace_size(L.OP_KV_ATTENTION, 3, 4, 2, 128, n) == 0
+    huge = cache(rows=2 << 31)
+    assert attend(lib, kc=huge, vc=huge) == L.UNSUPPORTED       # 2^31 tokens of 2 heads
+    many = cache(rows=65536 * 16, cols=64)
+    assert attend(lib, kc=many, vc=many, heads=65536, q_heads=65536, ld_q=1 << 22, ld_out=1 << 22, pages=1,
+                  ld_table=1, page=16) == L.UNSUPPORTED
+    assert attend(lib, n=1 << 30, seqs=1 << 30) == L.UNSUPPORTED  # 2^32 rows of queries
+
+
+def test_device_tensors_only(lib):
+    """A tensor of the host is refused before anything is launched on its address."""
+    import torch
+
+    import precision_moe_gemm_amd as nv
+    t = nv.NVFP4Tensor.empty(4, 64, 1, "cpu")
+    with pytest.raises((ValueError, AssertionError, RuntimeError)):
+        nv.nvfp4_audit_scales(t)
+    with pytest.raises(ValueError):
+        nv._stream("cpu")
+    with pytest.raises(ValueError):
+        nv._stream(torch.device("cpu"))
+
+
 NORM = dict(x=P(4096), ld_x=64, res=P(8192), ld_res=64, w=P(64), eps=1e-6, rows=3, cols=64, sum=P(12288), ld_sum=64,
             y=P(16384), ld_y=64, fp8=P(20480), e8=P(24576))
 

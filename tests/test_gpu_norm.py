@@ -78,6 +78,22 @@ def test_strides(orc, rows):
     assert (out[:, :16] == 9).all() and (out[:, 1040:] == 9).all()
 
 
+@pytest.mark.parametrize("cols", [32, 64, 96, 128, 160, 224, 256, 288])
+@pytest.mark.parametrize("rows", [1, 7, 33, 20001])
+def test_narrow_rows(orc, rows, cols):
+    """Several rows to a wave: odd numbers of them, strided, in place, without a residual or a weight."""
+    x, res, w = make(rows, cols, cols + rows)
+    step(f"narrow {rows} x {cols}")
+    check(orc, x, res, w, 1e-6, nv.mxfp8_add_rmsnorm(x, res, w, 1e-6, want_y=True))
+    check(orc, x, None, None, 1e-6, nv.mxfp8_add_rmsnorm(x, None, None, 1e-6, want_y=True))
+    wide = torch.full((rows, 2 * cols + 24), 9.0, dtype=torch.bfloat16, device=DEV)
+    wide[:, 8:8 + cols], wide[:, 16 + cols:16 + 2 * cols] = x, res
+    got = nv.mxfp8_add_rmsnorm(wide[:, 8:8 + cols], wide[:, 16 + cols:16 + 2 * cols], w, 1e-6,
+                               sum_out=wide[:, 8:8 + cols])
+    check(orc, x, res, w, 1e-6, got)
+    assert (wide[:, :8] == 9).all() and (wide[:, 8 + cols:16 + cols] == 9).all() and (wide[:, 16 + 2 * cols:] == 9).all()
+
+
 def test_extreme_rows(orc):
     """Zero rows (eps keeps them finite), tiny rows, huge rows, one element only."""
     x, res, w = make(6, 256, 4)
