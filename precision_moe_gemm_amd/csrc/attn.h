@@ -827,11 +827,11 @@ attn_rows_kernel(AttnArgs a)
 }
 
 // Joins what the shares left of one tile of rows (blockIdx.x) for one KV head
-// (blockIdx.y), in the order of the tokens, with the running maximum and sum
-// of the walk.  A wave holds a piece of 4 output elements per lane:
-// `pieces` waves take different pieces, the others (few tiles with many
-// parts each) different runs of the parts, joined through shared memory.
-// What it takes is the latency of three dependent reads and the launch.
+// (blockIdx.y), 16 of its rows (blockIdx.z % NT), in the order of the tokens,
+// with the running maximum and sum of the walk.  A wave holds a piece of 4
+// output elements per lane; `pieces` waves of a workgroup take different
+// pieces, the others different runs of the parts, joined through shared
+// memory.  What it takes is the latency of three dependent reads and the launch.
 template <int D, int NT>
 __global__ void __launch_bounds__(1024)
 attn_combine_kernel(AttnArgs a, int pieces)
@@ -856,57 +856,52 @@ attn_combine_kernel(AttnArgs a, int pieces)
     };
     const int runs = waves / pieces, pw = wave / pieces;
     const int run = (parts + runs - 1) / runs, p0 = pw * run, p1 = p0 + run < parts ? p0 + run : parts;
-#pragma unroll 1
-    for (int t = 0; t < NT; t++) {
-        const int rows = attn_part_rows(tile.nq * a.group - tile.row0 - 16 * t);
-        if (rows == 0)
-            break;
-        const bool in = n < rows;
-        const int off = t * (D / 4 + 2) * 64 + g * rows + (in ? n : 0);
-        const int r = tile.row0 + 16 * t + n;
-        const int i = r / a.group, head = h * a.group + r - i * a.group;
-        const int64_t token = tile.q0 + i;
-        for (int c0 = blockIdx.z * pieces; c0 < D / 16; c0 += gridDim.z * pieces) {
-            const int c = c0 + wave % pieces;  // (D / 16 is a multiple of pieces)
-            const int k = c / (D / 64), dd = 4 * (c - k * (D / 64));
-            float m = kAttnLow, l = 0.0f;
-            float4_t o = (float4_t){0, 0, 0, 0};
-            auto join = [&](float om, float ol, float4_t oo) {
-                const float now = __builtin_fmaxf(m, om);
-                const float f = __builtin_amdgcn_exp2f(m - now), q = __builtin_amdgcn_exp2f(om - now);
-                l = l * f + ol * q;
-                o = o * f + oo * q;
-                m = now;
-            };
+    const int t = blockIdx.z % NT;
+    const int rows = attn_part_rows(tile.nq * a.group - tile.row0 - 16 * t);
+    if (rows == 0)
+        return;
+    const bool in = n < rows;
+    const int off = t * (D / 4 + 2) * 64 + g * rows + (in ? n : 0);
+    const int r = tile.row0 + 16 * t + n;
+    const int i = r / a.group, head = h * a.group + r - i * a.group;
+    const int64_t token = tile.q0 + i;
+    const int c = blockIdx.z / NT * pieces + wave % pieces;
+    const int k = c / (D / 64), dd = 4 * (c - k * (D / 64));
+    float m = kAttnLow, l = 0.0f;
+    float4_t o = (float4_t){0, 0, 0, 0};
+    auto join = [&](float om, float ol, float4_t oo) {
+        const float now = __builtin_fmaxf(m, om);
+        const float f = __builtin_amdgcn_exp2f(m - now), q = __builtin_amdgcn_exp2f(om - now);
+        l = l * f + ol * q;
+        o = o * f + oo * q;
+        m = now;
+    };
 #pragma unroll 4
-            for (int p = p0; p < p1; p++) {
-                const float* src = part(p) + off;
-                float4_t oo;
+    for (int p = p0; p < p1; p++) {
+        const float* src = part(p) + off;
+        float4_t oo;
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    oo[j] = src[(2 + 4 * (dd + j) + k) * 4 * rows];
-                join(src[0], src[4 * rows], oo);
-            }
-            if (runs > 1) {
-                sum[wave][lane] = o;
-                red[wave][lane] = (float2_t){m, l};
-                __syncthreads();
-                for (int q = 1; q < runs && pw == 0; q++) {
-                    const float2_t ml = red[wave + q * pieces][lane];
-                    join(ml.x, ml.y, sum[wave + q * pieces][lane]);
-                }
-                __syncthreads();  // sum and red are written again
-            }
-            if (pw != 0 || !in)
-                continue;
-            const float scale = l != 0.0f ? vg / l : 0.0f;
-            *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
-                (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
-            if (a.lse && c == 0 && g == 0)
-                a.lse[token * (a.kv_heads * a.group) + head] =
-                    l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+        for (int j = 0; j < 4; j++)
+            oo[j] = src[(2 + 4 * (dd + j) + k) * 4 * rows];
+        join(src[0], src[4 * rows], oo);
+    }
+    if (runs > 1) {
+        sum[wave][lane] = o;
+        red[wave][lane] = (float2_t){m, l};
+        __syncthreads();
+        for (int q = 1; q < runs && pw == 0; q++) {
+            const float2_t ml = red[wave + q * pieces][lane];
+            join(ml.x, ml.y, sum[wave + q * pieces][lane]);
         }
     }
+    if (pw != 0 || !in)
+        return;
+    const float scale = l != 0.0f ? vg / l : 0.0f;
+    *(u32x2*)(a.out + token * a.ld_out + (int64_t)head * D + (4 * g + k) * (D / 16) + dd) =
+        (u32x2){pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale)};
+    if (a.lse && c == 0 && g == 0)
+        a.lse[token * (a.kv_heads * a.group) + head] =
+            l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
 }
 
 // ---------------------------------------------------------------------------

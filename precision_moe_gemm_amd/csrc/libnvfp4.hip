@@ -224,6 +224,12 @@ int64_t attention_tiles(int64_t n, int64_t group, int64_t seqs, int rows)
     return (n * group + std::min(n, seqs) * (rows - 1)) / rows;
 }
 
+// The same of one call, exact where every sequence has one token.
+int64_t attention_tiles(const AttnArgs& a, int rows)
+{
+    return a.cu_q ? attention_tiles(a.n, a.group, a.seqs, rows) : a.seqs * ceil_div(a.group, rows);
+}
+
 size_t attention_tiles_bytes(int64_t n, int64_t group, int64_t seqs)
 {
     return align256((size_t)(1 + attention_tiles(n, group, seqs, 16)) * sizeof(AttnTile));
@@ -255,17 +261,24 @@ size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64
 // 1024 threads per tile; what does not fit goes to the tile kernel.
 bool attention_rows_fit(const AttnArgs& a, int rows)
 {
-    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, rows);
+    const int64_t tiles = attention_tiles(a, rows);
     return tiles <= 0x3FFFFF && tiles * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) <= 0x7FFFFFFF;
 }
 
+// Few short sequences: a workgroup per tile and KV head, its waves side by
+// side over the tokens, and no second launch.  One sequence, 8 KV heads of 128:
+// 256 tokens 9.4 us (14.3 with shares), 700 tokens 11.8 (14.3), 1500 tokens 16.2
+// (14.5), 6000 tokens 38 (16); 32 sequences (256 workgroups) of 700 tokens 14.0
+// (17.5), 64 of them 24.9 (21.4).
 constexpr int64_t kWholeTiles = 256, kWholeTokens = 1024;
+// Waves of the joining launch (four per SIMD).  4 sequences of 4000 tokens, 8 KV
+// heads of 128: 22 us together with the shares (24 with 8192 waves, 23 with
+// 16384); 8 sequences, 4 heads of 256: 32, 32, 35; 64 sequences: 70, 70, 72.
+constexpr int64_t kJoinWaves = 4096;
 template <int D, int NT>
 nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
 {
-    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, 16 * NT);
-    // Few short sequences: a workgroup per tile and KV head, its waves side by
-    // side over the tokens, and no second launch.
+    const int64_t tiles = attention_tiles(a, 16 * NT);
     if (tiles * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens) {
         a.whole = 1;
         a.head_lanes = 1;
@@ -278,11 +291,15 @@ nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK)
         return s;
-    // many tiles: four waves, each other pieces of the output; few tiles (of
-    // many parts each): 16 waves share the parts of one piece
-    const bool many = tiles * a.kv_heads >= 128;
-    attn_combine_kernel<D, NT><<<dim3((unsigned)tiles, a.kv_heads, many ? 1 : D / 16), many ? 256 : 1024, 0, st>>>(
-        a, many ? 4 : 1);
+    // a wave for every piece of 4 output elements per lane, 16 rows and KV head, and several on runs of its
+    // parts while there are not too many
+    const int64_t items = tiles * a.kv_heads * NT * (D / 16);
+    int runs = 1;
+    while (runs < 16 && items * runs * 2 <= kJoinWaves)
+        runs *= 2;
+    const int pieces = runs >= 4 ? 1 : 4 / runs;
+    attn_combine_kernel<D, NT><<<dim3((unsigned)tiles, a.kv_heads, NT * (D / 16 / pieces)), 64 * runs * pieces, 0, st>>>(
+        a, pieces);
     return launch_status();
 }
 
@@ -290,7 +307,7 @@ template <int D, int NW>
 nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
 {
     constexpr int ROWS = 32 * NW;
-    const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, ROWS);
+    const int64_t tiles = attention_tiles(a, ROWS);
     if (tiles * a.kv_heads * 64 * NW > 0xFFFFFFFF)  // threads of one dimension of a launch
         return NVFP4_ERR_UNSUPPORTED;
     const int64_t splits = std::min(attention_tile_splits(tiles, a.kv_heads),
@@ -310,8 +327,15 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
     a.workers = attention_workers(a.kv_heads, a.head_lanes);
     if (max_q * a.group <= 16 && attention_rows_fit(a, 16))
         return launch_attention_rows<D, 1>(a, st);
-    if (max_q * a.group <= 32 && attention_rows_fit(a, 32))
+    // (rows of a sequence and KV head, GPU time of row tiles of 32 and of tiles of 128 rows, 8 KV heads of 128,
+    // 4000 tokens: 64 rows of 8 sequences 34 and 74 us, of 64 sequences 126 and 235; 128 rows of 64 sequences 245
+    // and 239; one sequence 20 and 20.  With 32 KV heads and 64 prompts of 60 tokens 57 and 73, of 120 122 and
+    // 112, 100 rows on 600 tokens of heads of 64 151 and 99.  Tiles of 16 rows for 32: 107 us where one of 32
+    // takes 80, 64 sequences)
+    if (max_q * a.group <= 64 && attention_rows_fit(a, 32))
         return launch_attention_rows<D, 2>(a, st);
+    // (128 rows of 64 sequences, 128-row tiles and 256-row ones: 239 and 257 us, heads of 64 72 and 85; 192 rows
+    // 391 and 283, 107 and 89)
     if (D == 256 || max_q * a.group <= 128)
         return launch_attention_tiles<D, 4>(a, st);
     if constexpr (D < 256)

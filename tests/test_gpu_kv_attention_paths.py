@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 def widen(c, tokens):
     """The same sequences in a table of at least `tokens` tokens per row, the new entries no pages."""
     t = c["table"]
-    wide = torch.full((t.shape[0], -(-tokens // c["page"])), -1, dtype=torch.int32, device=DEV)
+    wide = torch.full((t.shape[0], max(t.shape[1], -(-tokens // c["page"]))), -1, dtype=torch.int32, device=DEV)
     wide[:, :t.shape[1]] = t
     c["table"] = wide
     return c
@@ -44,6 +44,16 @@ def test_shares_drafts(D):
     check(c, f"shares drafts window D={D}", window=37)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kvh,group,seqs,m", [(4, 4, 1, 20000), (8, 4, 4, 3000), (2, 20, 3, 2000), (1, 1, 12, 1500),
+                                              (16, 2, 40, 200), (3, 30, 20, 150)])
+def test_joins(D, kvh, group, seqs, m):
+    """Few tiles of many parts, many of few: every split of the joining launch's waves."""
+    r = np.random.default_rng(seqs)
+    lens = [int(v) for v in r.integers(m // 2, m, seqs)]
+    check(widen(make_case([1] * seqs, lens, kvh, group, D, 16, seed=m, decode=True), 1040), f"joins {D} {kvh} {group} {m}")
+
+
 @pytest.mark.parametrize("seqs", [64, 65, 129, 5000])
 def test_many_sequences(seqs):
     r = np.random.default_rng(seqs)
@@ -56,9 +66,9 @@ def test_many_sequences(seqs):
 
 
 # ---- tiles ---------------------------------------------------------------------
-# (rows of the longest sequence times group: 33 .. 128 and more than 128)
+# (rows of the longest sequence times group: 40, then 128 and more)
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("heads,group,most", [(1, 1, 40), (2, 2, 64), (3, 1, 129), (1, 5, 70), (4, 8, 17), (1, 40, 4)])
+@pytest.mark.parametrize("heads,group,most", [(1, 1, 40), (2, 1, 65), (2, 2, 64), (3, 1, 129), (1, 5, 70), (4, 8, 17), (1, 40, 4)])
 @pytest.mark.parametrize("page", [16, 48])
 def test_tiles(D, heads, group, most, page):
     q_lens = [most, 1, 0, most - 1, 3]
@@ -75,7 +85,7 @@ def test_tiles_lengths(D, most):
     check(make_case([most] + [2, most // 2] * 4, kv_lens, 1, 2, D, 32, seed=D + most), f"tiles lengths {D} {most}")
 
 
-@pytest.mark.parametrize("D,rows", [(64, 40), (64, 200), (128, 40), (128, 200), (256, 70)])
+@pytest.mark.parametrize("D,rows", [(64, 40), (64, 100), (64, 200), (128, 40), (128, 100), (128, 200), (256, 70)])
 @pytest.mark.parametrize("page", [16, 112, 256])
 def test_tiles_split(D, rows, page):
     """Few tiles on a long context: its tokens are split over workgroups and joined."""
@@ -191,7 +201,7 @@ def test_a_row_with_nan_spoils_itself_alone(q_lens, kv_lens):
 
 
 CALLS = [([1] * 5, [1500, 30, 1, 0, 700], "shares"), ([1] * 5, [90, 30, 1, 0, 64], "one launch"),
-         ([60, 2, 0, 30, 5], [900, 30, 1, 50, 70], "128-row tiles"), ([200, 2, 0, 30, 5], [2500, 30, 1, 50, 70], "split")]
+         ([15, 2, 0, 9, 5], [1500, 30, 1, 50, 70], "shares of 32 rows"), ([60, 2, 0, 30, 5], [900, 30, 1, 50, 70], "128-row tiles"), ([200, 2, 0, 30, 5], [2500, 30, 1, 50, 70], "split")]
 
 
 @pytest.mark.parametrize("q_lens,kv_lens,what", CALLS)
