@@ -221,6 +221,20 @@ def test_workspace_is_enough_and_may_hold_anything(q_lens, kv_lens, what):
         call(c, ws=buf[:need - 1])
 
 
+@pytest.mark.parametrize("seqs,group", [(100, 70), (128, 65), (60, 129), (3, 100)])
+def test_workspace_of_single_tokens_of_wide_groups(seqs, group):
+    """Tiles of many rows without cu_q: what is counted exactly and what the workspace was sized for."""
+    c = widen(make_case([1] * seqs, [int(v) for v in np.random.default_rng(1).integers(1, 60, seqs)], 1, group, 64, 16,
+                        seed=group, decode=True), 4096)
+    need = nv.nvfp4_workspace_size(_lib.OP_KV_ATTENTION, seqs, group, 1, 64, seqs)
+    buf = torch.full((need + (1 << 22),), 0xFF, dtype=torch.uint8, device=DEV)
+    step(f"single tokens of {seqs} sequences, group {group}")
+    out, lse = call(c, ws=buf[:need])
+    torch.cuda.synchronize()
+    assert (buf[need:] == 0xFF).all()
+    assert_attention(out, lse, reference(c), f"single tokens, group {group}")
+
+
 @pytest.mark.parametrize("q_lens,kv_lens,what", CALLS)
 def test_graph_replays(q_lens, kv_lens, what):
     """Captured once; lengths, pages and offsets are read at every replay."""
