@@ -136,8 +136,12 @@ NVFP4_DEV void attn_limits(const AttnArgs& a, const AttnSeq& s, int i, int* star
     *start = b;
 }
 
-NVFP4_DEV AttnSeq attn_seq_uniform(const AttnArgs& a, int b)
+// Sequence b, uniform.  own: lane l's sequence l, where there are at most 64.
+NVFP4_DEV AttnSeq attn_seq_uniform(const AttnArgs& a, const AttnSeq& own, int b)
 {
+    if (a.seqs <= 64)
+        return AttnSeq{__builtin_amdgcn_readlane(own.q0, b), __builtin_amdgcn_readlane(own.nq, b),
+                       __builtin_amdgcn_readlane(own.kv, b), false};
     const AttnSeq s = attn_seq(a, b);
     return AttnSeq{uniform(s.q0), uniform(s.nq), uniform(s.kv), s.down};
 }
@@ -210,6 +214,8 @@ NVFP4_DEV AttnFound attn_find(const AttnScan& s, int seqs, int u, Count count)
     f.before.tiles = __builtin_amdgcn_readlane(s.before.tiles, l);
     f.before.units = __builtin_amdgcn_readlane(s.before.units, l);
     f.at = u - f.before.units;
+    if (per == 1)
+        return f;
     for (;;) {
         const AttnCount c = count(f.seq);
         const int tiles = uniform(c.tiles), units = uniform(c.tiles * c.units);
@@ -747,8 +753,10 @@ attn_rows_kernel(AttnArgs a)
     const int blocks = a.kv_heads / hl;
     const int hb = blockIdx.x / 8 % blocks, w = blockIdx.x / (8 * blocks) * 8 + blockIdx.x % 8;
     const int h = hb * hl + wave % hl, tl = wave / hl;
+    AttnSeq own{0, 0, 0, false};
     auto count = [&](int b) {
-        AttnCount c = attn_count<D, NT>(a, attn_seq(a, b));
+        own = attn_seq(a, b);
+        AttnCount c = attn_count<D, NT>(a, own);
         c.units = a.whole ? 1 : c.units;  // whole tiles: w counts tiles
         return c;
     };
@@ -762,7 +770,7 @@ attn_rows_kernel(AttnArgs a)
     const int u1 = (int)((w + 1) * total / shares);
     AttnFound f = attn_find(scan, a.seqs, u, count);
     while (u < u1) {
-        const AttnSeq s = attn_seq_uniform(a, f.seq);
+        const AttnSeq s = attn_seq_uniform(a, own, f.seq);
         AttnCount c = attn_count<D, NT>(a, s);
         const int units = c.units;
         c.units = a.whole ? 1 : c.units;
@@ -1044,9 +1052,10 @@ attn_tile_kernel(AttnArgs a)
     // ---- the tile: heavy ones first (causal tiles grow towards the end)
     const int h = blockIdx.x % a.kv_heads;
     const int split = blockIdx.y;
+    AttnSeq own{0, 0, 0, false};
     auto count = [&](int b) ATTN_INLINE {
-        const AttnSeq s = attn_seq(a, b);
-        return AttnCount{(s.nq * a.group + ROWS - 1) / ROWS, 1, s.down};
+        own = attn_seq(a, b);
+        return AttnCount{(own.nq * a.group + ROWS - 1) / ROWS, 1, own.down};
     };
     const AttnScan scan = attn_scan(a.seqs, count);
     const int slot = blockIdx.x / a.kv_heads;
@@ -1056,7 +1065,7 @@ attn_tile_kernel(AttnArgs a)
         return;
     const int tile_no = scan.units - 1 - slot;
     const AttnFound f = attn_find(scan, a.seqs, tile_no, count);
-    const AttnSeq s = attn_seq_uniform(a, f.seq);
+    const AttnSeq s = attn_seq_uniform(a, own, f.seq);
     const int row0 = f.at * ROWS;
     int lo0, hi0, lo1, hi1;  // tokens of the tile's first and last row
     const int last = (row0 + ROWS - 1) / a.group;
@@ -1077,19 +1086,25 @@ attn_tile_kernel(AttnArgs a)
     int start = 0, end = 0;
     if (in)
         attn_limits(a, s, qi, &start, &end);
-    half8_t q[D / 16];
-    float c1;
+    // (D = 256: converted behind the first requests of K and V, 2218 against 2257 us for 2048 rows on 30720
+    // tokens; at D = 128 registers then spill and 4096 rows take 167 instead of 150)
+    u32x4 qw[D / 16];
     {
         const uint16_t* src = a.q + (int64_t)(s.q0 + (in ? qi : 0)) * a.ld_q + (int64_t)(h * a.group + hh) * D + 8 * e;
-        u32x4 w[D / 16];
-        uint32_t am = 0;
 #pragma unroll
         for (int c = 0; c < D / 16; c++) {
-            w[c] = (u32x4){0, 0, 0, 0};
+            qw[c] = (u32x4){0, 0, 0, 0};
             if (in)
-                w[c] = *(const u32x4*)(src + 16 * c);
-            am = umax_u32(am, absmax_bits8(w[c]));
+                qw[c] = *(const u32x4*)(src + 16 * c);
         }
+    }
+    half8_t q[D / 16];
+    float c1;
+    auto convert = [&]() ATTN_INLINE {
+        uint32_t am = 0;
+#pragma unroll
+        for (int c = 0; c < D / 16; c++)
+            am = umax_u32(am, absmax_bits8(qw[c]));
         am = umax_u32(am, (uint32_t)__shfl_xor((int)am, 32, 64));
         const int ex = am ? __builtin_amdgcn_frexp_expf(__uint_as_float(am << 16)) - 1 : 0;
         c1 = __builtin_fmaxf(__builtin_ldexpf(a.scale_log2 * *a.k_global, ex), 1e-37f);
@@ -1097,10 +1112,12 @@ attn_tile_kernel(AttnArgs a)
         for (int c = 0; c < D / 16; c++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                q[c][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[c][j]), -ex);
-                q[c][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[c][j]), -ex);
+                q[c][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(qw[c][j]), -ex);
+                q[c][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(qw[c][j]), -ex);
             }
-    }
+    };
+    if constexpr (D < 256)
+        convert();
     // ---- staging: the thread's elements of K (token kt, elements kd .. + kK)
     // and of V (tokens 4 vt .. + 4, elements vd .. + kV)
     const int32_t* table = a.table + f.seq * a.ld_table;
@@ -1318,14 +1335,20 @@ attn_tile_kernel(AttnArgs a)
             pages_k(b0);
             load_k(b0);
             pages_k(b0 + 1);
-            for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE { decode_k(zero, u); });
-            load_k(b0 + 1);
-            pages_k(b0 + 2);
         }
         if constexpr (has_v) {
             pages_v(b0);
             load_v(b0);
             pages_v(b0 + 1);
+        }
+        if constexpr (D == 256)
+            convert();
+        if constexpr (has_k) {
+            for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE { decode_k(zero, u); });
+            load_k(b0 + 1);
+            pages_k(b0 + 2);
+        }
+        if constexpr (has_v) {
             interleave();
             for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE { decode_v(zero, u); });
             load_v(b0 + 1);
