@@ -507,6 +507,13 @@ def _heads(t, what, device):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
+def _caches_on(device, *caches):
+    """Every part of the caches on `device`: the library gets their addresses alone."""
+    for t in caches:
+        if t.packed.device != device or t.scales.device != device or t.global_.device != device:
+            raise ValueError("the caches' codes, scales and globals must be on the operands' device")
+
+
 def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, slots: torch.Tensor,
                     k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, positions: torch.Tensor | None = None,
                     cos_sin: torch.Tensor | None = None, interleaved: bool = False,
@@ -518,6 +525,7 @@ def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Ten
     Without cos_sin nothing is rotated.  heads: KV heads of the caches, needed
     only when neither k nor v is given."""
     device = k_cache.device
+    _caches_on(device, k_cache, v_cache)
     kv = k if k is not None else v
     if kv is not None:
         heads = kv.shape[1]
@@ -573,8 +581,9 @@ def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tens
     device = q.device
     ld_q = _heads(q, "q", device)
     n, q_heads, D = q.shape
-    if k_cache.device != device or v_cache.device != device or k_cache.cols != D:
-        raise ValueError("q and the caches must be on one device, with one head_dim")
+    _caches_on(device, k_cache, v_cache)
+    if k_cache.cols != D:
+        raise ValueError("q and the caches must have one head_dim")
     _operand(block_table, "block_table", torch.int32, 2, device)
     _operand(kv_lens, "kv_lens", torch.int32, 1, device)
     seqs, pages = block_table.shape
