@@ -561,7 +561,8 @@ nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, 
  * each.  With the data checks on, q and the globals are checked, not the
  * caches' scales: unwritten pages may hold anything.  D is 64, 128 or 256 and
  * page_size % 16 == 0 on this build, and a cache has fewer than 2^31 tokens
- * (else NVFP4_ERR_UNSUPPORTED); scale finite and positive.
+ * (else NVFP4_ERR_UNSUPPORTED); with D = 256 the caches' scales are 16-byte
+ * aligned; scale finite and positive.
  */
 nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads,
                                 const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,

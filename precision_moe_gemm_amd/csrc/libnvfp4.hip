@@ -2270,6 +2270,9 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
         !aligned(lse, 4) || (pages_per_seq > 0 && !block_table) || !aligned(block_table, 4))
         return NVFP4_ERR_INVALID_ARG;
+    // (a row's 16 scale bytes are one copy)
+    if (D == 256 && (!aligned(k_cache->scales, 16) || !aligned(v_cache->scales, 16)))
+        return NVFP4_ERR_INVALID_ARG;
     const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_ATTENTION, n, q_heads, kv_heads, D, seqs);
     if (need > 0 && (!ws || !aligned(ws, 256)))
         return NVFP4_ERR_INVALID_ARG;
