@@ -541,7 +541,8 @@ nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, 
  * A row that sees no token (an empty sequence, a position before 0) gets
  * zeros and lse = -inf.  Rows behind the last sequence are not written.
  *   q: bf16 [n, q_heads, D], token stride ld_q elements (a multiple of 8);
- *   out: bf16, the same shape, token stride ld_out (not q: no overlap);
+ *   out: bf16, the same shape, token stride ld_out; it shares no element with q
+ *   (else NVFP4_ERR_INVALID_ARG; side by side in one buffer they may lie);
  *   lse: fp32 [n, q_heads] or NULL;
  *   max_q: the most query rows that a sequence has (it chooses the kernel; a
  *   wrong one costs speed, not results); 1 when cu_q is NULL;

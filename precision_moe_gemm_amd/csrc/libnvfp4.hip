@@ -89,6 +89,26 @@ nvfp4_status check_tensor(const nvfp4_tensor* t, bool need_global = true, bool t
     return NVFP4_OK;
 }
 
+// Whether two bf16 matrices of `rows` rows (wa and wb elements each, at strides
+// lda >= wa and ldb >= wb) share an element: side by side in one wider buffer
+// they do not.
+bool rows_share(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows)
+{
+    if (!a || !b || rows < 1)
+        return false;
+    if ((uintptr_t)a > (uintptr_t)b)
+        return rows_share(b, ldb, wb, a, lda, wa, rows);
+    const __int128 la = (__int128)lda * 2, lb = (__int128)ldb * 2, ea = wa * 2, eb = wb * 2;  // bytes
+    __int128 at = (uintptr_t)b - (uintptr_t)a;  // a row of b, from a's first
+    // with one stride the rows of b meet those of a as b's first does, only fewer of them
+    for (int64_t j = 0; j < (la == lb ? 1 : rows) && at < (rows - 1) * la + ea; j++, at += lb) {
+        const __int128 i = (at + eb - 1) / la;  // the last row of a that begins before its end
+        if ((i < rows ? i : rows - 1) * la + ea > at)
+            return true;
+    }
+    return false;
+}
+
 // ---------------------------------------------------------------- checks
 // The data-check switch (nvfp4_set_checks): its start value comes from the
 // NVFP4_CHECK environment variable when the library is loaded, else from the
@@ -2269,6 +2289,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
         return NVFP4_ERR_SHAPE;
     if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
         !aligned(lse, 4) || (pages_per_seq > 0 && !block_table) || !aligned(block_table, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows_share(q, ld_q, q_heads * D, out, ld_out, q_heads * D, n))
         return NVFP4_ERR_INVALID_ARG;
     // (a row's 16 scale bytes are one copy)
     if (D == 256 && (!aligned(k_cache->scales, 16) || !aligned(v_cache->scales, 16)))

@@ -17,3 +17,23 @@ def test_attention_scales_of_256_wide_heads_are_copied_16_bytes_at_a_time(lib):
     for cols in (64, 128):  # copies of 4 bytes
         odd = cache(cols=cols, scales=8196)
         assert attend(lib, kc=odd, vc=odd, **short) == L.WORKSPACE, cols
+
+
+def test_attention_out_must_not_share_memory_with_q(lib):
+    """Workgroups write their rows while others still read q: 3 rows of 512 elements, 1024 bytes each."""
+    from precision_moe_gemm_amd import _lib as L
+    q = 1 << 16
+    for out, ld_q, ld_out in ((q, 512, 512), (q + 16, 512, 512), (q - 16, 512, 512), (q + 1024, 512, 512),
+                              (q + 3056, 512, 512), (q - 3056, 512, 512), (q, 1024, 512), (q, 512, 1024),
+                              (q + 2048, 1024, 1024),              # out's row 0 is q's row 1
+                              (q + 1040, 1024, 1024),              # out's row 0 ends in q's row 1
+                              (q - 2064, 1024, 1024),              # q's row 0 begins in out's row 1
+                              (q + 1024, 1024, 512), (q - 1024, 512, 1024), (q + 1024, 1536, 1088)):
+        assert attend(lib, q=P(q), out=P(out), ld_q=ld_q, ld_out=ld_out, ws_bytes=0) == L.INVALID_ARG, (out - q, ld_q, ld_out)
+    for out, ld_q, ld_out in ((q + 3072, 512, 512), (q - 3072, 512, 512), (q + 1024, 1024, 1024),
+                              (q - 1024, 1024, 1024),              # side by side in one wide buffer
+                              (q + 5120, 1024, 1024),              # from out's second row on, behind q's last one
+                              (q + 3072, 1 << 40, 512), (q + 1024, 2048, 512), (q - 1024, 512, 2048),
+                              (q + 1024, 1024, 2048)):
+        assert attend(lib, q=P(q), out=P(out), ld_q=ld_q, ld_out=ld_out, ws_bytes=0) == L.WORKSPACE, (out - q, ld_q, ld_out)
+    assert attend(lib, q=P(q), out=P(q + 16), ld_q=(1 << 62) + 8, ld_out=(1 << 62) + 8, ws_bytes=0) == L.INVALID_ARG
