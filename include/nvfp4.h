@@ -258,8 +258,9 @@ nvfp4_status mxfp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int6
  *   fp8, e8m0 = mxfp8_quantize(y)
  * x, residual, sum, y: bf16 [rows, cols] with row strides ld_* (elements,
  * multiples of 8, 16-byte aligned); weight: bf16 [cols].  Outputs, each
- * optional: r to sum (may be x or residual itself with the same stride), y,
- * and the pair fp8 [rows, cols] / e8m0 [rows, cols/32] (both or neither).  The
+ * optional: r to sum (may be x or residual itself with the same stride; one
+ * that shares an element with them otherwise: NVFP4_ERR_INVALID_ARG), y, and
+ * the pair fp8 [rows, cols] / e8m0 [rows, cols/32] (both or neither).  The
  * result does not depend on how a row is split over threads.  cols % 32 == 0
  * (else NVFP4_ERR_SHAPE) and cols <= 65536 on this build (else UNSUPPORTED);
  * eps >= 0.  An all-zero row with eps = 0 gives unspecified output.
@@ -507,10 +508,11 @@ nvfp4_status nvfp4_kv_dequant(const nvfp4_tensor* k_cache, const nvfp4_tensor* v
  * q, k, v may be slices of one projection's output: ld_* are token strides in
  * elements (multiples of 8); heads are contiguous.  q may be NULL (then
  * q_heads and q_out are not used), so may k or v.  q_out may be q itself with
- * the same stride; no other buffers may overlap.  cos_sin: fp32 [max_pos,
- * rot_dim], 16-byte aligned; positions int32 [n], slots int64 [n] on the
- * device.  A negative slot stores nothing (padding); its q row is still
- * rotated.  A slot past the cache or, on a token with a slot, a position
+ * the same stride; no other buffers may overlap (a q_out that shares an
+ * element with k or v, or with q otherwise: NVFP4_ERR_INVALID_ARG).  cos_sin:
+ * fp32 [max_pos, rot_dim], 16-byte aligned; positions int32 [n], slots int64
+ * [n] on the device.  A negative slot stores nothing (padding); its q row is
+ * still rotated.  A slot past the cache or, on a token with a slot, a position
  * outside [0, max_pos) raises the sticky NVFP4_ERR_RANGE and stores nothing;
  * the q row of a token with such a position becomes zeros.  Slots that are not
  * negative must differ from each other: of two tokens with the same slot,

@@ -109,6 +109,12 @@ bool rows_share(const void* a, int64_t lda, int64_t wa, const void* b, int64_t l
     return false;
 }
 
+// The same of an output that may also be the input itself, row for row.
+bool rows_clash(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t width, int64_t rows)
+{
+    return !(out == in && (ld_out == ld_in || rows <= 1)) && rows_share(out, ld_out, width, in, ld_in, width, rows);
+}
+
 // ---------------------------------------------------------------- checks
 // The data-check switch (nvfp4_set_checks): its start value comes from the
 // NVFP4_CHECK environment variable when the library is loaded, else from the
@@ -2214,6 +2220,10 @@ nvfp4_status nvfp4_kv_append(const void* q, int64_t ld_q, int32_t q_heads, const
         return NVFP4_ERR_INVALID_ARG;
     if (rot_dim > 0 && (!positions || !aligned(positions, 4) || !cos_sin || !aligned(cos_sin, 16)))
         return NVFP4_ERR_INVALID_ARG;
+    if (q && (rows_clash(q_out, ld_qout, q, ld_q, heads[0] * D, n) ||
+              rows_share(q_out, ld_qout, heads[0] * D, k, ld_k, heads[1] * D, n) ||
+              rows_share(q_out, ld_qout, heads[0] * D, v, ld_v, heads[2] * D, n)))
+        return NVFP4_ERR_INVALID_ARG;
     if (rot_dim > 0 && max_pos < 1)
         return NVFP4_ERR_SHAPE;
     if (heads[0] + 2 * (int64_t)kv_heads > 65536)
@@ -2367,6 +2377,8 @@ nvfp4_status mxfp8_add_rmsnorm(const void* x, int64_t ld_x, const void* residual
         return NVFP4_ERR_UNSUPPORTED;
     if (!x || !aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) ||
         !aligned(y, 16) || !aligned(fp8, 16))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows_clash(sum, ld_sum, x, ld_x, cols, rows) || rows_clash(sum, ld_sum, residual, ld_res, cols, rows))
         return NVFP4_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = (const u32x4*)x;

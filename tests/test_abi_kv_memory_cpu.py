@@ -37,3 +37,38 @@ def test_attention_out_must_not_share_memory_with_q(lib):
                               (q + 1024, 1024, 2048)):
         assert attend(lib, q=P(q), out=P(out), ld_q=ld_q, ld_out=ld_out, ws_bytes=0) == L.WORKSPACE, (out - q, ld_q, ld_out)
     assert attend(lib, q=P(q), out=P(q + 16), ld_q=(1 << 62) + 8, ld_out=(1 << 62) + 8, ws_bytes=0) == L.INVALID_ARG
+
+
+def test_append_q_out_is_q_or_lies_elsewhere(lib):
+    """One unit of a row is read and written by one thread: in place is right with q's own stride alone."""
+    from precision_moe_gemm_amd import _lib as L
+    rows = dict(q=P(1 << 16), k=P(1 << 17), v=P(1 << 18))
+
+    def refused(**kw):
+        """The next check (an empty table of angles) stops what is not refused for its place."""
+        s = append(lib, **dict(rows, max_pos=0, **kw))
+        assert s in (L.INVALID_ARG, L.SHAPE)
+        return s == L.INVALID_ARG
+
+    assert not refused(q_out=P(1 << 16))
+    assert refused(q_out=P(1 << 16), ld_qo=1024)
+    assert refused(q_out=P((1 << 16) + 16)) and refused(q_out=P((1 << 16) - 16))
+    assert refused(q_out=P(1 << 17)) and refused(q_out=P((1 << 17) + 16), ld_qo=512)
+    assert refused(q_out=P((1 << 18) - 3056))
+    assert not refused(q_out=P((1 << 17) - 3072)) and not refused(q_out=P((1 << 17) + 1536))
+    rows = dict(q=P(1 << 16), k=P((1 << 16) + 1024), v=P((1 << 16) + 1536), ld_q=1024, ld_k=1024, ld_v=1024)
+    assert not refused(q_out=P(1 << 16), ld_qo=1024)             # the three parts of one projection's rows
+    assert refused(q_out=P((1 << 16) + 1024), ld_qo=1024)
+    assert not refused(q_out=P(1 << 16), ld_qo=2048, n=1)        # one row has no stride
+
+
+def test_norm_sum_is_an_input_or_lies_elsewhere(lib):
+    """(What is not refused runs on the GPU: the sum in place of either, and beside them in one buffer.)"""
+    from precision_moe_gemm_amd import _lib as L
+    x, res = 1 << 16, 1 << 17  # 3 rows of 64 elements
+    at = dict(x=P(x), res=P(res), y=P(1 << 18), fp8=P(1 << 19), e8=P(1 << 20))
+    for base in (x, res):
+        for off, ld in ((0, 72), (0, 128), (16, 64), (-16, 64), (128, 64), (-256, 64), (368, 64), (-368, 64), (256, 96)):
+            assert norm(lib, **at, sum=P(base + off), ld_sum=ld) == L.INVALID_ARG, (base, off, ld)
+    assert norm(lib, **dict(at, res=P(x + 16)), sum=P(x)) == L.INVALID_ARG   # x itself, but part of the residual
+    assert norm(lib, **at, sum=P(x + 256), ld_x=128, ld_sum=128) == L.INVALID_ARG
