@@ -263,7 +263,10 @@ nvfp4_status mxfp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int6
  * the pair fp8 [rows, cols] / e8m0 [rows, cols/32] (both or neither).  The
  * result does not depend on how a row is split over threads.  cols % 32 == 0
  * (else NVFP4_ERR_SHAPE) and cols <= 65536 on this build (else UNSUPPORTED);
- * eps >= 0.  An all-zero row with eps = 0 gives unspecified output.
+ * eps >= 0.  An all-zero row with eps = 0 gives unspecified output.  A row
+ * with an infinite r has inv = 0: y is 0 where r is finite and NaN where it is
+ * not; a NaN in r makes its row NaN.  (The codes of a block with a NaN are
+ * unspecified.)
  */
 nvfp4_status mxfp8_add_rmsnorm(const void* x_bf16, int64_t ld_x, const void* residual_bf16, int64_t ld_res,
                                const void* weight_bf16, double eps, int64_t rows, int64_t cols, void* sum_bf16,

@@ -40,6 +40,8 @@ NVFP4_DEV float inv_sqrt_f64(double v)
 {
     if (!(v > 0.0))
         return v == 0.0 ? __builtin_inff() : __builtin_nanf("");
+    if (v == __builtin_inf())  // (frexp and the steps below give NaN)
+        return 0.0f;
     int e = 0;
     const double m = __builtin_frexp(v, &e);  // m in [0.5, 1)
     const int half = e >> 1;                  // v = (m * 2^(e & 1)) * 2^(2 half)
