@@ -2250,17 +2250,16 @@ nvfp4_status nvfp4_kv_append(const void* q, int64_t ld_q, int32_t q_heads, const
     a.cpr = (int)(D / 8);
     a.rot = rot_dim;
     a.interleaved = interleaved != 0;
-    launch_kv_append(a, S(stream));
-    nvfp4_status s = launch_status();
-    if (s == NVFP4_OK && checks_on()) {
+    if (checks_on()) {
+        // (before the launch: the rotated q may take the place of q)
         for (int j = 0; j < 3; j++)
             if (src[j])
                 check_bf16(src[j], n, heads[j] * D, ld[j], S(stream));
         check_globals(k_cache->global, 1, S(stream));
         check_globals(v_cache->global, 1, S(stream));
-        s = launch_status();
     }
-    return s;
+    launch_kv_append(a, S(stream));
+    return launch_status();
 }
 
 nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
@@ -2396,17 +2395,16 @@ nvfp4_status mxfp8_add_rmsnorm(const void* x, int64_t ld_x, const void* residual
     a.chunks = (int)(cols / 8);
     a.cols = (double)cols;
     a.eps = eps;
-    launch_add_rmsnorm(a, S(stream));
-    nvfp4_status s = launch_status();
-    if (s == NVFP4_OK && checks_on()) {
+    if (checks_on()) {
+        // (before the launch: the sum may take the place of x or the residual)
         check_bf16(x, rows, cols, ld_x, S(stream));
         if (residual)
             check_bf16(residual, rows, cols, ld_res, S(stream));
         if (weight)
             check_bf16(weight, 1, cols, cols, S(stream));
-        s = launch_status();
     }
-    return s;
+    launch_add_rmsnorm(a, S(stream));
+    return launch_status();
 }
 
 }  // extern "C"
