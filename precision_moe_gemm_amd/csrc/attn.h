@@ -57,7 +57,7 @@ struct AttnArgs {
     int page_shift;          // t / page = (t / 8) * page_mul >> (32 + page_shift)
     uint32_t page_mul;
     int kv_heads, group;     // group: query heads per KV head
-    float scale_log2;        // scale * log2(e)
+    double scale_log2;       // scale * log2(e)
     int causal, window;
     uint16_t* out;           // [n, heads, D], token stride ld_out
     int64_t ld_out;
@@ -75,9 +75,54 @@ template <int D, int NT>
 constexpr int attn_waves() { return D * NT <= 256 ? 8 : 4; }
 typedef __attribute__((address_space(3))) void* attn_lds_t;
 constexpr int kAttnStep = 32;            // tokens of one step
-constexpr float kAttnLow = -1e30f;       // running maximum of a row that has seen nothing
+constexpr float kAttnLow = -3.402823466e38f;  // running maximum of a row that has seen nothing
 constexpr float kAttnLazy = 8.0f;        // growth of the maximum (log 2) that is let pass
 constexpr float kAttnLift = 7.0f;        // p is held times 2^7, at most 2^15 (f16 holds 65504)
+
+// Far scores.  Scores are s * c1 with a factor c1 per row, and weights
+// 2^(s c1 + lift) come from one fused multiply-add, whose exact product exceeds
+// the rounded one that the maximum was taken from by up to half a step of it,
+// as the lift is off by half a step: together with the 2^15 that a weight may
+// be, at most 2^15.5 while the maximum stays within 2^22, but past f16's
+// largest value from 2^24 on.  A row whose maximum leaves that range therefore
+// keeps its scores in units of 2^k (c1 and m times 2^-k, m back inside).  What
+// lies 32 units below the maximum counts for nothing, so this is as if a score
+// were off by up to 32 2^k, 2^-16 of the largest: past 2^22, fp32 holds its own
+// sum of D products to D 2^-24 of that.
+
+// c1 and k of a row whose q was divided by 2^e, in 64 bits, as the factors alone
+// may pass fp32's range.  c1 stays above zero (-inf times it stays -inf) and
+// below 2^100 (|s| is below 2^21).
+NVFP4_DEV float attn_factor(double scale_log2, float k_global, int e, int* k)
+{
+    const double x = __builtin_ldexp(scale_log2 * k_global, e);
+    const int over = __builtin_amdgcn_frexp_exp(x) - 100;
+    *k = over > 0 ? over : 0;
+    return x < 1e-37 ? 1e-37f : (float)__builtin_ldexp(x, -*k);
+}
+
+// The running maximum m of a row becomes `now`: what l and o are multiplied by.
+NVFP4_DEV float attn_grow(float now, float* m, float* c1, int* k)
+{
+    float f = __builtin_amdgcn_exp2f(*m - now);
+    const bool far = (__builtin_fabsf(now) > 4194304.0f || *k > 0) && now > kAttnLow;
+    if (__any(far)) {
+        f = __builtin_amdgcn_exp2f(__builtin_ldexpf(*m - now, *k));
+        const int over = now != 0.0f ? __builtin_amdgcn_frexp_expf(now) + *k - 22 : 0;
+        const int by = far ? *k - (over > 0 ? over : 0) : 0;
+        now = __builtin_ldexpf(now, by);
+        *c1 = __builtin_ldexpf(*c1, by);
+        *k -= by;
+    }
+    *m = now;
+    return f;
+}
+
+// The maximum itself, at most fp32's largest value.
+NVFP4_DEV float attn_whole(float m, int k)
+{
+    return __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(m, k), kAttnLow), -kAttnLow);
+}
 
 // One sequence as the kernels see it: bad lengths are cut to what exists and
 // raise NVFP4_ERR_RANGE.  down: its end lies before its start.
@@ -326,6 +371,7 @@ struct AttnWave {
     half8_t q[NT][D / 32];
     float4_t o[NT][D / 16];
     float m[NT], l[NT], c1[NT];
+    int k[NT];  // m, c1 and the scores are in units of 2^k
     int start[NT], end[NT];
     // the lane's part of the copies: its place in 16 tokens' codes (of the even and the odd copies of a
     // half) and its row among the 32 tokens' scales
@@ -364,8 +410,7 @@ struct AttnWave {
             // the row's largest magnitude is f * 2^e, f in [1, 2)
             const float top = __uint_as_float(am << 16);
             const int e = am ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;
-            // (kept above zero: -inf times it stays -inf)
-            c1[t] = __builtin_fmaxf(__builtin_ldexpf(a.scale_log2 * kg, e), 1e-37f);
+            c1[t] = attn_factor(a.scale_log2, kg, e, &k[t]);
 #pragma unroll
             for (int c = 0; c < D / 32; c++)
 #pragma unroll
@@ -478,9 +523,7 @@ struct AttnWave {
             if (__any(top > m[t] + kAttnLazy)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                const float now = __builtin_fmaxf(m[t], top);
-                const float f = __builtin_amdgcn_exp2f(m[t] - now);
-                m[t] = now;
+                const float f = attn_grow(__builtin_fmaxf(m[t], top), &m[t], &c1[t], &k[t]);
                 l[t] *= f;
 #pragma unroll
                 for (int dd = 0; dd < D / 16; dd++)
@@ -611,11 +654,12 @@ struct AttnWave {
         wait_vm<0>();
     }
 
-    // the sums of the lane groups
+    // the sums of the lane groups, the maxima in units of 1
     NVFP4_DEV void close()
     {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
+            m[t] = attn_whole(m[t], k[t]);
             l[t] += __shfl_xor(l[t], 16, 64);
             l[t] += __shfl_xor(l[t], 32, 64);
         }
@@ -1100,6 +1144,12 @@ attn_tile_kernel(AttnArgs a)
     }
     half8_t q[D / 16];
     float c1;
+    // m, c1 and the scores are in units of 2^k.  It is read where the maximum grows only, and kept in shared
+    // memory where a register more spills (D = 128, eight waves: 4096 rows 155 us, 152 so)
+    __shared__ int row_k[D < 256 ? ROWS : 1];
+    int one_k;
+    int* const k2 = D < 256 ? row_k + 32 * wave + col : &one_k;
+    *k2 = 0;
     auto convert = [&]() ATTN_INLINE {
         uint32_t am = 0;
 #pragma unroll
@@ -1107,7 +1157,7 @@ attn_tile_kernel(AttnArgs a)
             am = umax_u32(am, absmax_bits8(qw[c]));
         am = umax_u32(am, (uint32_t)__shfl_xor((int)am, 32, 64));
         const int ex = am ? __builtin_amdgcn_frexp_expf(__uint_as_float(am << 16)) - 1 : 0;
-        c1 = __builtin_fmaxf(__builtin_ldexpf(a.scale_log2 * *a.k_global, ex), 1e-37f);
+        c1 = attn_factor(a.scale_log2, *a.k_global, ex, k2);
 #pragma unroll
         for (int c = 0; c < D / 16; c++)
 #pragma unroll
@@ -1286,9 +1336,7 @@ attn_tile_kernel(AttnArgs a)
         top *= c1;
         if (__any(top > m + kAttnLazy)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-            const float now = __builtin_fmaxf(m, top);
-            const float g = __builtin_amdgcn_exp2f(m - now);
-            m = now;
+            const float g = attn_grow(__builtin_fmaxf(m, top), &m, &c1, k2);
             l *= g;
             if constexpr (D < 256) {
 #pragma unroll
@@ -1402,6 +1450,7 @@ attn_tile_kernel(AttnArgs a)
     }
     if (bad)
         raise_error(NVFP4_ERR_RANGE);
+    m = attn_whole(m, *k2);
     l += __shfl_xor(l, 32, 64);
     const int head = h * a.group + hh;
     const int64_t token = s.q0 + qi;

@@ -2334,7 +2334,7 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
     a.kv_heads = kv_heads;
     a.group = q_heads / kv_heads;
-    a.scale_log2 = scale * 1.44269504089f;
+    a.scale_log2 = (double)scale * 1.4426950408889634;
     a.causal = causal != 0;
     a.window = window;
     a.out = (uint16_t*)out;
