@@ -507,6 +507,13 @@ def _heads(t, what, device):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
+def _int32(**numbers):
+    """Refuse what the C ABI's 32-bit integers would take modulo 2^32."""
+    for name, v in numbers.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
+
+
 def _caches_on(device, *caches):
     """Every part of the caches on `device`: the library gets their addresses alone."""
     for t in caches:
@@ -523,14 +530,17 @@ def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Ten
     sines), quantize k and v into the caches at slots (int64 [n]; negative: not
     stored).  Returns the rotated q (q_out, new if omitted; may be q).
     Without cos_sin nothing is rotated.  heads: KV heads of the caches, needed
-    only when neither k nor v is given."""
+    only when neither k nor v is given (else it must be theirs)."""
     device = k_cache.device
     _caches_on(device, k_cache, v_cache)
     kv = k if k is not None else v
     if kv is not None:
+        if heads is not None and heads != kv.shape[1]:
+            raise ValueError(f"heads: {heads} where k or v has {kv.shape[1]}")
         heads = kv.shape[1]
     elif heads is None:
         raise ValueError("heads is needed without k and v")
+    _int32(heads=heads)
     n = slots.numel()
     ld = [0, 0, 0]
     for j, (name, t) in enumerate((("q", q), ("k", k), ("v", v))):
@@ -597,6 +607,7 @@ def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tens
             raise ValueError("cu_q: seqs + 1 entries")
     if max_q is None:
         max_q = 1 if cu_q is None else n
+    _int32(heads=heads, page_size=page_size, max_q=max_q, window=window)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
     ld_out = _heads(out, "out", device)

@@ -71,3 +71,24 @@ def test_a_cache_that_lies_elsewhere(calls, call, which, parts):
     with pytest.raises(ValueError):
         call(**{which: cache(**parts)})
     assert calls == []
+
+
+@pytest.mark.parametrize("name", ["heads", "page_size", "max_q", "window"])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 16, -(1 << 32) + 16])
+def test_numbers_past_32_bits(calls, name, value):
+    """The C types would take them modulo 2^32: a window of 2^32 + 16 as one of 16."""
+    with pytest.raises(ValueError):
+        attend(**{name: value})
+    assert calls == []
+
+
+def test_heads_that_contradict_the_operands(calls):
+    for kw in (dict(heads=4), dict(heads=1, k=None), dict(heads=3, v=None)):
+        with pytest.raises(ValueError):
+            append(**kw)
+    with pytest.raises(ValueError):
+        append(q=dev(N, 4, D), k=None, v=None, heads=(1 << 32) + 2)
+    assert calls == []
+    append(heads=2)
+    append(heads=2, v=None)
+    assert calls == ["nvfp4_kv_append"] * 2
