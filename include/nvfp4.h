@@ -257,16 +257,16 @@ nvfp4_status mxfp8_quantize(const void* x_bf16, int64_t rows, int64_t cols, int6
  *   y   = bf16((r * inv) * weight)           (fp32 steps; weight NULL: ones)
  *   fp8, e8m0 = mxfp8_quantize(y)
  * x, residual, sum, y: bf16 [rows, cols] with row strides ld_* (elements,
- * multiples of 8, 16-byte aligned); weight: bf16 [cols].  Outputs, each
- * optional: r to sum (may be x or residual itself with the same stride; one
- * that shares an element with them otherwise: NVFP4_ERR_INVALID_ARG), y, and
+ * multiples of 8); weight: bf16 [cols]; these and fp8 16-byte aligned.  Outputs,
+ * each optional: r to sum (may be x or residual itself with the same stride;
+ * one that shares an element with them otherwise: NVFP4_ERR_INVALID_ARG), y, and
  * the pair fp8 [rows, cols] / e8m0 [rows, cols/32] (both or neither).  The
- * result does not depend on how a row is split over threads.  cols % 32 == 0
- * (else NVFP4_ERR_SHAPE) and cols <= 65536 on this build (else UNSUPPORTED);
- * eps >= 0.  An all-zero row with eps = 0 gives unspecified output.  A row
- * with an infinite r has inv = 0: y is 0 where r is finite and NaN where it is
- * not; a NaN in r makes its row NaN.  (The codes of a block with a NaN are
- * unspecified.)
+ * order of a row's sum is set by cols: a row gives the same bytes in every call.
+ * cols % 32 == 0 (else NVFP4_ERR_SHAPE) and cols <= 65536 on this build (else
+ * UNSUPPORTED); eps >= 0.  An all-zero row with eps = 0 gives unspecified
+ * output.  A row with an infinite r has inv = 0: y is 0 where r is finite and
+ * NaN where it is not; a NaN in r makes its row NaN.  (The codes of a block with
+ * a NaN are unspecified.)
  */
 nvfp4_status mxfp8_add_rmsnorm(const void* x_bf16, int64_t ld_x, const void* residual_bf16, int64_t ld_res,
                                const void* weight_bf16, double eps, int64_t rows, int64_t cols, void* sum_bf16,
@@ -520,7 +520,8 @@ nvfp4_status nvfp4_kv_dequant(const nvfp4_tensor* k_cache, const nvfp4_tensor* v
  * the q row of a token with such a position becomes zeros.  Slots that are not
  * negative must differ from each other: of two tokens with the same slot,
  * that slot's content is unspecified (other slots are not affected).
- * D % 32 == 0, D <= 4096 and rot_dim % 32 == 0, rot_dim <= D on this build.
+ * D % 32 == 0, D <= 4096, rot_dim % 32 == 0, rot_dim <= D and at most 65536
+ * heads in all (q_heads + 2 kv_heads) on this build.
  */
 nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, const void* k_bf16, int64_t ld_k,
                              const void* v_bf16, int64_t ld_v, int32_t kv_heads, int64_t n, const int64_t* slots,

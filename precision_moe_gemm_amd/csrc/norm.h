@@ -8,9 +8,11 @@
 //   y = bf16((r * i) * w)                     (fp32 steps)
 //   codes, scales = mxfp8_quantize(y)
 //
-// r^2 of a bf16 value is exact in fp32, and the sum of a row in fp64 is off
-// by less than 2^-40 of itself in any order: i is the same fp32 value for
-// every split of the row over threads, and with it every byte of the output.
+// r^2 of a bf16 value is exact, and a row's sum in fp64 is off by at most
+// cols 2^-53 of itself in any order (2^-37 at 65536 columns): i is the fp32
+// value of the exact sum but where that lies so close to a border of fp32's
+// rounding.  The order of the sum is set by cols alone, so a row gives the same
+// bytes in every call.
 #pragma once
 #include "common.h"
 #include "mx8.h"
