@@ -560,8 +560,8 @@ nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, 
  * Products are exact and summed in fp32 (q is held in f16 relative to its
  * row's largest element, p in f16); results do not depend on anything but the
  * arguments.  Scores may have any finite size: where the largest of a row lies
- * past 2^22 ln 2 they count as known to 2^-16 of it, and an lse past fp32's
- * range is that range's end.  An entry that is not a page of the cache, a
+ * past 2^22 ln 2 they count as known to 2^-16 of it, and what lies past fp32's
+ * range (in units of ln 2) counts as that range's end.  An entry that is not a page of the cache, a
  * kv_lens[b] outside [0, pages_per_seq * page_size] or a cu_q that decreases or
  * leaves [0, n] raises the sticky NVFP4_ERR_RANGE: such a page's tokens are
  * skipped, such a length or offset is cut, and a cu_q that decreases writes

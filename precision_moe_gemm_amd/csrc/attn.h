@@ -108,7 +108,10 @@ NVFP4_DEV float attn_grow(float now, float* m, float* c1, int* k)
     const bool far = (__builtin_fabsf(now) > 4194304.0f || *k > 0) && now > kAttnLow;
     if (__any(far)) {
         f = __builtin_amdgcn_exp2f(__builtin_ldexpf(*m - now, *k));
-        const int over = now != 0.0f ? __builtin_amdgcn_frexp_expf(now) + *k - 22 : 0;
+        // (a maximum near zero under a factor past 2^100: later scores must not overflow)
+        int over = now != 0.0f ? __builtin_amdgcn_frexp_expf(now) - 22 : -1000;
+        const int most = __builtin_amdgcn_frexp_expf(*c1) - 100;
+        over = (over > most ? over : most) + *k;
         const int by = far ? *k - (over > 0 ? over : 0) : 0;
         now = __builtin_ldexpf(now, by);
         *c1 = __builtin_ldexpf(*c1, by);

@@ -75,9 +75,12 @@ def check(c, keys, scale, what, spread=False):
     out, lse = call(c, scale=scale)
     torch.cuda.synchronize()
     wo, wl, tol, ltol = reference(c, keys, float(torch.tensor(scale, dtype=torch.float32)), spread)
-    bad = ~((out.cpu().double() - wo).abs() <= tol)
+    past = wl.abs() > 2.35e38  # (fp32's largest value times ln 2: scores past it count as it)
+    assert out.isfinite().all() and lse.isfinite().all(), what
+    assert (lse.cpu()[past].sign() == wl[past].sign()).all(), what
+    bad = ~((out.cpu().double() - wo).abs() <= tol) & ~past[..., None]
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[0].tolist())
-    bad = ~((lse.cpu().double() - wl).abs() <= ltol)
+    bad = ~((lse.cpu().double() - wl).abs() <= ltol) & ~past
     assert not bad.any(), (what, "lse", int(bad.sum()), bad.nonzero()[0].tolist())
 
 
@@ -143,3 +146,20 @@ def test_factors_whose_product_alone_is_ordinary(scale, q, glob):
         c["q"].zero_()
         c["q"][..., 3] = q
         check(c, keys * glob, scale, f"scale {scale}, q {q}, global {glob}, {what}", spread=True)
+
+
+@pytest.mark.parametrize("e,scale", [(10, 0.125), (60, 0.125), (110, 1.0), (127, 1.0), (127, 100.0)])
+@pytest.mark.parametrize("q_lens,kv_lens,decode,what", CALLS)
+def test_a_maximum_of_zero_before_far_scores(q_lens, kv_lens, decode, what, e, scale):
+    """Keys of zero first: a maximum of 0 under a factor of up to 2^134, then scores that leave it behind or stay
+    far below it."""
+    c = make_case(q_lens, kv_lens, 2, 4, 128, 16, seed=e, decode=decode)
+    keys = random_keys(c, 4)
+    keys[:, :max(kv_lens) * 2 // 3] = 0
+    keys[:, 0] = 0
+    place_keys(c, keys)
+    g = torch.Generator().manual_seed(6)
+    sign = torch.where(torch.rand(c["q"].shape[:2], generator=g) < 0.5, -1.0, 1.0)
+    c["q"].zero_()
+    c["q"][..., 3] = (sign * 2.0 ** e).to(DEV)
+    check(c, keys, scale, f"zeros before scores of 2^{e}, scale {scale}, {what}")
