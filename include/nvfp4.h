@@ -550,7 +550,8 @@ nvfp4_status nvfp4_kv_append(const void* q_bf16, int64_t ld_q, int32_t q_heads, 
  *   out: bf16, the same shape, token stride ld_out; it shares no element with q
  *   (else NVFP4_ERR_INVALID_ARG; side by side in one buffer they may lie);
  *   lse: fp32 [n, q_heads] or NULL;
- *   max_q: the most query rows that a sequence has (it chooses the kernel; a
+ *   max_q: the most query rows that a sequence has (it chooses the kernel, one
+ *   for all sequences: long chunks and single tokens are faster in two calls; a
  *   wrong one costs speed, not results); 1 when cu_q is NULL;
  *   block_table: int32 [seqs, pages_per_seq], row stride ld_table.  Entries of
  *   pages with no token that a row sees (past the sequence's length, before

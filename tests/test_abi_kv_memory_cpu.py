@@ -1,6 +1,12 @@
 """Refusals of the cache and norm operators that concern where their operands lie: found on the host, before
-any launch (no GPU here)."""
-from tests.test_abi_kv_cpu import P, append, attend, cache, lib, norm  # noqa: F401  (lib: the fixture)
+any launch (no GPU here), and the same under the sanitizer build of the host layer."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from tests.test_abi_kv_cpu import P, ROOT, append, attend, cache, lib, norm  # noqa: F401  (lib: the fixture)
 
 
 def test_attention_scales_of_256_wide_heads_are_copied_16_bytes_at_a_time(lib):
@@ -72,3 +78,17 @@ def test_norm_sum_is_an_input_or_lies_elsewhere(lib):
             assert norm(lib, **at, sum=P(base + off), ld_sum=ld) == L.INVALID_ARG, (base, off, ld)
     assert norm(lib, **dict(at, res=P(x + 16)), sum=P(x)) == L.INVALID_ARG   # x itself, but part of the residual
     assert norm(lib, **at, sum=P(x + 256), ld_x=128, ld_sum=128) == L.INVALID_ARG
+
+
+@pytest.mark.skipif("NVFP4_LIB_PATH" in os.environ, reason="this run is the sanitized one")
+def test_these_under_asan_ubsan():
+    from precision_moe_gemm_amd import build
+    env = dict(os.environ, LD_PRELOAD=build.sanitizer_runtime(), NVFP4_LIB_PATH=build.build_sanitized(),
+               ASAN_OPTIONS="detect_leaks=0:halt_on_error=1:abort_on_error=0",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "not gpu",
+                        "tests/test_abi_kv_memory_cpu.py"], cwd=ROOT, env=env, capture_output=True, text=True,
+                       timeout=900)
+    out = r.stdout + r.stderr
+    assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
+    assert r.returncode == 0, out[-4000:]
