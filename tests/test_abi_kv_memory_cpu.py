@@ -28,18 +28,18 @@ def test_attention_scales_of_256_wide_heads_are_copied_16_bytes_at_a_time(lib):
 def test_attention_out_must_not_share_memory_with_q(lib):
     """Workgroups write their rows while others still read q: 3 rows of 512 elements, 1024 bytes each."""
     from precision_moe_gemm_amd import _lib as L
-    q = 1 << 16
+    q, end = 1 << 16, 3 * 1024  # (end: behind three dense rows)
     for out, ld_q, ld_out in ((q, 512, 512), (q + 16, 512, 512), (q - 16, 512, 512), (q + 1024, 512, 512),
-                              (q + 3056, 512, 512), (q - 3056, 512, 512), (q, 1024, 512), (q, 512, 1024),
+                              (q + end - 16, 512, 512), (q - end + 16, 512, 512), (q, 1024, 512), (q, 512, 1024),
                               (q + 2048, 1024, 1024),              # out's row 0 is q's row 1
                               (q + 1040, 1024, 1024),              # out's row 0 ends in q's row 1
                               (q - 2064, 1024, 1024),              # q's row 0 begins in out's row 1
                               (q + 1024, 1024, 512), (q - 1024, 512, 1024), (q + 1024, 1536, 1088)):
         assert attend(lib, q=P(q), out=P(out), ld_q=ld_q, ld_out=ld_out, ws_bytes=0) == L.INVALID_ARG, (out - q, ld_q, ld_out)
-    for out, ld_q, ld_out in ((q + 3072, 512, 512), (q - 3072, 512, 512), (q + 1024, 1024, 1024),
+    for out, ld_q, ld_out in ((q + end, 512, 512), (q - end, 512, 512), (q + 1024, 1024, 1024),
                               (q - 1024, 1024, 1024),              # side by side in one wide buffer
                               (q + 5120, 1024, 1024),              # from out's second row on, behind q's last one
-                              (q + 3072, 1 << 40, 512), (q + 1024, 2048, 512), (q - 1024, 512, 2048),
+                              (q + end, 1 << 40, 512), (q + 1024, 2048, 512), (q - 1024, 512, 2048),
                               (q + 1024, 1024, 2048)):
         assert attend(lib, q=P(q), out=P(out), ld_q=ld_q, ld_out=ld_out, ws_bytes=0) == L.WORKSPACE, (out - q, ld_q, ld_out)
     assert attend(lib, q=P(q), out=P(q + 16), ld_q=(1 << 62) + 8, ld_out=(1 << 62) + 8, ws_bytes=0) == L.INVALID_ARG
@@ -60,8 +60,8 @@ def test_append_q_out_is_q_or_lies_elsewhere(lib):
     assert refused(q_out=P(1 << 16), ld_qo=1024)
     assert refused(q_out=P((1 << 16) + 16)) and refused(q_out=P((1 << 16) - 16))
     assert refused(q_out=P(1 << 17)) and refused(q_out=P((1 << 17) + 16), ld_qo=512)
-    assert refused(q_out=P((1 << 18) - 3056))
-    assert not refused(q_out=P((1 << 17) - 3072)) and not refused(q_out=P((1 << 17) + 1536))
+    assert refused(q_out=P((1 << 18) - 3 * 1024 + 16))
+    assert not refused(q_out=P((1 << 17) - 3 * 1024)) and not refused(q_out=P((1 << 17) + 1536))
     rows = dict(q=P(1 << 16), k=P((1 << 16) + 1024), v=P((1 << 16) + 1536), ld_q=1024, ld_k=1024, ld_v=1024)
     assert not refused(q_out=P(1 << 16), ld_qo=1024)             # the three parts of one projection's rows
     assert refused(q_out=P((1 << 16) + 1024), ld_qo=1024)
