@@ -122,7 +122,8 @@ enum {
     NVFP4_OP_MOE = 3,      /* nvfp4_moe_grouped_gemm                */
     NVFP4_OP_MOE_ROUTE = 4, /* nvfp4_moe_route / the staged GEMMs   */
     NVFP4_OP_MX_MOE = 5,    /* mx_moe_w4a8                          */
-    NVFP4_OP_KV_ATTENTION = 6 /* nvfp4_kv_attention                 */
+    NVFP4_OP_KV_ATTENTION = 6, /* nvfp4_kv_attention, .._tree       */
+    NVFP4_OP_KV_WEIGHTS = 7   /* nvfp4_kv_weights                   */
 };
 
 /* Bytes of `ws` an operation needs.  Unused arguments may be 0:
@@ -130,8 +131,8 @@ enum {
  *   GEMM: T = M (rows of A), H = K, I = N (rows of W); non-zero only for
  *         few-row shapes whose K is split over several workgroups.
  *   MOE, MOE_ROUTE: T tokens, k slots, E experts, H hidden, I intermediate.
- *   KV_ATTENTION: T = n (query rows), k = q_heads, E = kv_heads, H = head_dim,
- *         I = seqs. */
+ *   KV_ATTENTION, KV_WEIGHTS: T = n (query rows), k = q_heads, E = kv_heads,
+ *         H = head_dim, I = seqs. */
 size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 
 /*
@@ -581,6 +582,116 @@ nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ld_q, int64_t n, int
                                 int32_t page_size, const int32_t* kv_lens, const int32_t* cu_q, int32_t seqs,
                                 int32_t max_q, float scale, int32_t causal, int32_t window, void* out_bf16,
                                 int64_t ld_out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of trees of drafted tokens over a paged NVFP4 KV cache: as
+ * nvfp4_kv_attention, but for what a row sees.  The m query rows of a sequence
+ * are its last m tokens, the drafts (their keys and values are in the cache, in
+ * the order of the rows; each was rotated by its own position).  Row i sees the
+ * kv_lens[b] - m tokens before the drafts and those drafts j whose bit is set:
+ * bit j % 32 of word j / 32 of mask row cu_q[b] + i.  Usually these are its
+ * ancestors and itself, but nothing is implied: a row of zero bits sees no
+ * draft.  Bits of drafts that do not exist (j >= m) have no effect.  With window
+ * > 0 a row sees the last `window` of these tokens, in their order.
+ *   mask: uint32 [n, mask_words] on the device, row stride ld_mask words.  A
+ *   sequence with more than 32 * mask_words drafts raises the sticky
+ *   NVFP4_ERR_RANGE, and no row sees the drafts behind them.
+ * A sequence with fewer cached tokens than query rows has no tokens before the
+ * drafts, and of these only the last kv_lens[b].  Table entries of pages that lie
+ * wholly more than `window` tokens before the drafts may hold anything.
+ */
+nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads,
+                                     const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,
+                                     const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq,
+                                     int32_t page_size, const int32_t* kv_lens, const int32_t* cu_q, int32_t seqs,
+                                     int32_t max_q, const uint32_t* mask, int64_t ld_mask, int32_t mask_words,
+                                     float scale, int32_t window, void* out_bf16, int64_t ld_out, float* lse, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * The attention weight that each cached token receives, per KV head, added to
+ * what it has received before (for nvfp4_kv_select):
+ *   out[h, c] = w[h, c] + sum over the query rows r of the sequence that see
+ *     token t, and the query heads j of KV head h, of exp(scale * q[r, j] . k[t] - lse[r, j])
+ * with c the place of token t in the cache (page * page_size + its place in the
+ * page).  Sequences, query rows, causal and window are those of
+ * nvfp4_kv_attention, lse what it returned for these rows (fp32 [n, q_heads]).
+ * The rows' own tokens, the last of their sequence, have received nothing yet:
+ * w is not read there, nor anywhere if it is NULL (zeros).
+ *   weights (w): fp32 [kv_heads, tokens of the cache], row stride ld_weights;
+ *   weights_out: the same shape, row stride ld_out; it may be w itself with the
+ *   same stride (one that shares an element with w otherwise:
+ *   NVFP4_ERR_INVALID_ARG).  Written are the cached tokens of the call's sequences
+ *   only; in place, tokens before every row's window are left as they are.
+ *   max_q: as there (a wrong one costs speed, not results).
+ *   ws: nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs)
+ *   bytes, 256-byte aligned.
+ * Each of the weights counts as a number of [0, 1], a NaN as 0: rows of q with a
+ * NaN or infinity and rows with an lse that is not finite add nothing.  The order
+ * of a token's sum is set by the arguments: no atomics.  Scores past fp32's range
+ * (in units of ln 2) count as 0 or 1.  A page must belong to one sequence of the
+ * call; tokens of a page that two of them hold get the sum of either.  Lengths,
+ * offsets and entries that are out of range are handled as in
+ * nvfp4_kv_attention.  D is 64, 128 or 256 (scales 16-byte aligned with 256),
+ * page_size % 16 == 0, a row of the table covers at most 2^30 tokens on this
+ * build.
+ */
+nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads, const float* lse,
+                              const nvfp4_tensor* k_cache, int32_t kv_heads, const int32_t* block_table,
+                              int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                              const int32_t* cu_q, int32_t seqs, int32_t max_q, float scale, int32_t causal,
+                              int32_t window, const float* weights, int64_t ld_weights, float* weights_out,
+                              int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Which cached tokens each KV head of a sequence keeps when the sequence passes
+ * its budget, as the moves that close the gaps (for nvfp4_kv_move).  A sequence
+ * of at most `keep` tokens keeps them all.  Of a longer one, each KV head keeps
+ * `keep`: first those at a position below `sinks` or among the last `recent`
+ * before next_positions[b], then those with the largest weights; of equals (of
+ * tokens kept first, should there be too many, as well) the ones at the lowest
+ * place.  A NaN weight counts as -inf.  The i-th kept token at a place >= keep
+ * (in the order of the places) moves to the i-th place < keep whose token goes.
+ *   weights: fp32 [kv_heads, tokens], row stride ld_weights, as from
+ *   nvfp4_kv_weights; positions: int32, the same shape, row stride ld_positions,
+ *   each token's position in its sequence (moves mix the places), with
+ *   next_positions int32 [seqs], the position after the newest; or NULL: the
+ *   places are the positions, kv_lens[b] the next;
+ *   moves: int32 [seqs, kv_heads, cap, 2]: (source, destination) places, -1, -1
+ *   behind the last; cap >= min(keep, pages_per_seq * page_size - keep), else
+ *   NVFP4_ERR_SHAPE;
+ *   lens_out: int32 [seqs], min(kv_lens[b], keep); not kv_lens itself.
+ * Nothing is moved, and weights are not changed.  keep >= 1, sinks + recent <=
+ * keep (else NVFP4_ERR_INVALID_ARG).  A kv_lens[b] outside the table's places is
+ * cut and raises the sticky NVFP4_ERR_RANGE, as does an entry that is not a page
+ * of the cache: its tokens are the first to go.
+ */
+nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int32_t* positions, int64_t ld_positions,
+                             int32_t kv_heads, int64_t tokens, const int32_t* block_table, int64_t ld_table,
+                             int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                             const int32_t* next_positions, int32_t seqs, int32_t keep, int32_t sinks, int32_t recent,
+                             int32_t* moves, int32_t cap, int32_t* lens_out, void* stream);
+
+/*
+ * Move cached tokens within their sequences: K and V (codes and scales), and
+ * with weights or positions (fp32, int32 [kv_heads, tokens]; NULL: none) those
+ * too.  moves: int32 [seqs, lists, cap, 2], pairs (source, destination) of places
+ * of the sequence; lists is kv_heads (a list per KV head, as nvfp4_kv_select
+ * gives them) or 1 (one for all, as for the accepted path of a tree of drafts:
+ * draft path[i] of a sequence of kv drafts' tokens moves from kv - m + path[i] to
+ * kv - m + i).  A pair with a negative source moves nothing.
+ * With cap <= 256 every source of a list is read before any destination is
+ * written; longer lists must not write a place that they read (else its content
+ * is unspecified).  Destinations of a list differ from each other, else the
+ * place's content is that of any of them.  A place outside the table or in an
+ * entry that is not a page of the cache raises the sticky NVFP4_ERR_RANGE, and
+ * the pair moves nothing.  Pages that are moved within must belong to one
+ * sequence of the call.  D % 32 == 0 and D <= 4096 on this build.
+ */
+nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,
+                           const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq, int32_t page_size,
+                           int32_t seqs, const int32_t* moves, int32_t lists, int32_t cap, float* weights,
+                           int64_t ld_weights, int32_t* positions, int64_t ld_positions, void* stream);
 
 /*
  * Scale audit (page "Qwen3.8-Flash-Next-NVFP4", section 证据链: every block

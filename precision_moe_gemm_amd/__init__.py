@@ -24,7 +24,8 @@ __all__ = [
     "mxfp4_quantize", "mxfp4_to_nvfp4", "nvfp4_gemm", "nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_noalloc",
     "nvfp4_moe_route", "nvfp4_moe_gate_up", "nvfp4_moe_gate_up_q", "nvfp4_moe_down", "nvfp4_moe_combine",
     "nvfp4_gather_dequantize", "nvfp4_tile_scales", "nvfp4_gemm_w4a16", "nvfp4_moe_w4a16", "mxfp8_quantize", "mx_gemm_w4a8", "mx_moe_w4a8", "mx_moe_gate_up", "mx_moe_down",
-    "nvfp4_kv_quant", "nvfp4_kv_dequant", "nvfp4_kv_append", "nvfp4_kv_attention", "mxfp8_add_rmsnorm",
+    "nvfp4_kv_quant", "nvfp4_kv_dequant", "nvfp4_kv_append", "nvfp4_kv_attention", "nvfp4_kv_attention_tree",
+    "nvfp4_kv_weights", "nvfp4_kv_select", "nvfp4_kv_move", "mxfp8_add_rmsnorm",
     "nvfp4_audit_scales", "nvfp4_get_error", "nvfp4_set_checks",
     "nvfp4_recipe", "status_string",
 ]
@@ -576,38 +577,46 @@ def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Ten
     return q_out if q is not None else None
 
 
-def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int,
-                       block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int,
-                       cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
-                       causal: bool = True, window: int = 0, return_lse: bool = False,
-                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                       ws: torch.Tensor | None = None):
-    """Attention of q (bf16 [n, q_heads, D]) over the paged NVFP4 caches of
-    `heads` KV heads: block_table int32 [seqs, pages], kv_lens int32 [seqs].
-    cu_q (int32 [seqs + 1]) gives each sequence's query rows, one row per
-    sequence without it; max_q the most rows a sequence has (n if omitted).
-    scale: 1 / sqrt(D) if omitted.  Returns out (bf16, the shape of q), or
-    (out, lse float32 [n, q_heads]) with return_lse or lse."""
+def _pages(block_table, kv_lens, device):
+    """(sequences, pages of a table row, row stride) of a block table."""
+    _operand(block_table, "block_table", torch.int32, 2, device)
+    seqs, pages = block_table.shape
+    if kv_lens is not None:
+        _operand(kv_lens, "kv_lens", torch.int32, 1, device)
+        if kv_lens.numel() != seqs:
+            raise ValueError("kv_lens: one per row of block_table")
+    if seqs > 1 and block_table.stride(0) < pages:
+        raise ValueError("block_table: rows must not overlap")
+    return seqs, pages, block_table.stride(0) if seqs > 1 else pages
+
+
+def _query_rows(cu_q, seqs, device):
+    if cu_q is not None:
+        _operand(cu_q, "cu_q", torch.int32, 1, device)
+        if cu_q.numel() != seqs + 1:
+            raise ValueError("cu_q: seqs + 1 entries")
+
+
+def _kv_attention(q, k_cache, v_cache, heads, block_table, kv_lens, page_size, cu_q, max_q, mask, scale, causal, window,
+                  return_lse, out, lse, ws):
+    """The two attention calls (mask: that of a tree, or None)."""
     device = q.device
     ld_q = _heads(q, "q", device)
     n, q_heads, D = q.shape
     _caches_on(device, k_cache, v_cache)
     if k_cache.cols != D:
         raise ValueError("q and the caches must have one head_dim")
-    _operand(block_table, "block_table", torch.int32, 2, device)
-    _operand(kv_lens, "kv_lens", torch.int32, 1, device)
-    seqs, pages = block_table.shape
-    if kv_lens.numel() != seqs:
-        raise ValueError("kv_lens: one per row of block_table")
-    if seqs > 1 and block_table.stride(0) < pages:
-        raise ValueError("block_table: rows must not overlap")
-    if cu_q is not None:
-        _operand(cu_q, "cu_q", torch.int32, 1, device)
-        if cu_q.numel() != seqs + 1:
-            raise ValueError("cu_q: seqs + 1 entries")
+    seqs, pages, ld_table = _pages(block_table, kv_lens, device)
+    _query_rows(cu_q, seqs, device)
     if max_q is None:
         max_q = 1 if cu_q is None else n
     _int32(heads=heads, page_size=page_size, max_q=max_q, window=window)
+    if mask is not None:
+        _operand(mask, "mask", torch.int32, 2, device)
+        if mask.shape[0] != n:
+            raise ValueError("mask: a row per row of q")
+        if n > 1 and mask.stride(0) < mask.shape[1]:
+            raise ValueError("mask: rows must not overlap")
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
     ld_out = _heads(out, "out", device)
@@ -627,14 +636,167 @@ def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tens
         need = lib.nvfp4_workspace_size(_lib.OP_KV_ATTENTION, n, q_heads, heads, D, seqs)
         ws = _workspace(need, device) if need else None
     kc, vc = k_cache.c(), v_cache.c()
+    scale = D ** -0.5 if scale is None else scale
+    rows = (_ptr(q), ld_q, n, q_heads, ctypes.byref(kc), ctypes.byref(vc), heads, _ptr(block_table), ld_table, pages,
+            page_size, _ptr(kv_lens), _ptr(cu_q), seqs, max_q)
+    result = (window, _ptr(out), ld_out, _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(device))
     with _on(device):
-        st = lib.nvfp4_kv_attention(
-            _ptr(q), ld_q, n, q_heads, ctypes.byref(kc), ctypes.byref(vc), heads, _ptr(block_table),
-            block_table.stride(0) if seqs > 1 else pages, pages, page_size, _ptr(kv_lens), _ptr(cu_q), seqs, max_q,
-            D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), ld_out, _ptr(lse), _ptr(ws),
-            0 if ws is None else ws.numel(), _stream(device))
-    _check(st, "nvfp4_kv_attention")
+        if mask is None:
+            st = lib.nvfp4_kv_attention(*rows, scale, int(causal), *result)
+        else:
+            st = lib.nvfp4_kv_attention_tree(*rows, _ptr(mask), mask.stride(0) if n > 1 else mask.shape[1],
+                                             mask.shape[1], scale, *result)
+    _check(st, "nvfp4_kv_attention" if mask is None else "nvfp4_kv_attention_tree")
     return out if lse is None else (out, lse)
+
+
+def nvfp4_kv_attention(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int,
+                       block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int,
+                       cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
+                       causal: bool = True, window: int = 0, return_lse: bool = False,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None):
+    """Attention of q (bf16 [n, q_heads, D]) over the paged NVFP4 caches of
+    `heads` KV heads: block_table int32 [seqs, pages], kv_lens int32 [seqs].
+    cu_q (int32 [seqs + 1]) gives each sequence's query rows, one row per
+    sequence without it; max_q the most rows a sequence has (n if omitted).
+    scale: 1 / sqrt(D) if omitted.  Returns out (bf16, the shape of q), or
+    (out, lse float32 [n, q_heads]) with return_lse or lse."""
+    return _kv_attention(q, k_cache, v_cache, heads, block_table, kv_lens, page_size, cu_q, max_q, None, scale, causal,
+                         window, return_lse, out, lse, ws)
+
+
+def nvfp4_kv_attention_tree(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int,
+                            block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int,
+                            cu_q: torch.Tensor | None, mask: torch.Tensor, max_q: int | None = None,
+                            scale: float | None = None, window: int = 0, return_lse: bool = False,
+                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                            ws: torch.Tensor | None = None):
+    """nvfp4_kv_attention of trees of drafts: the query rows of a sequence are its
+    last cached tokens, and row i sees the tokens before them and the drafts of
+    its bits: bit j % 32 of mask[i, j // 32] for draft j (mask: int32 [n, words],
+    any row stride).  With window > 0 the last `window` of these."""
+    return _kv_attention(q, k_cache, v_cache, heads, block_table, kv_lens, page_size, cu_q, max_q, mask, scale, True,
+                         window, return_lse, out, lse, ws)
+
+
+def _by_token(t, what, dtype, heads, device):
+    """[heads, tokens of the cache], any row stride: the stride."""
+    _operand(t, what, dtype, 2, device)
+    if t.shape[0] != heads or (heads > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what}: a row of the cache's tokens per KV head is expected")
+    return t.stride(0) if heads > 1 else t.shape[1]
+
+
+def nvfp4_kv_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: NVFP4Tensor, heads: int, block_table: torch.Tensor,
+                     kv_lens: torch.Tensor, page_size: int, out: torch.Tensor, weights: torch.Tensor | None = None,
+                     cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
+                     causal: bool = True, window: int = 0, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Add the attention weight that each cached token receives from q (bf16 [n,
+    q_heads, D]) to weights (float32 [heads, cache tokens]; None: zeros) and write
+    it to out (the same shape; may be weights).  lse: what nvfp4_kv_attention
+    returned for these rows, whose arguments the others are."""
+    device = q.device
+    ld_q = _heads(q, "q", device)
+    n, q_heads, D = q.shape
+    _caches_on(device, k_cache)
+    if k_cache.cols != D:
+        raise ValueError("q and the cache must have one head_dim")
+    seqs, pages, ld_table = _pages(block_table, kv_lens, device)
+    _query_rows(cu_q, seqs, device)
+    if max_q is None:
+        max_q = 1 if cu_q is None else n
+    _int32(heads=heads, page_size=page_size, max_q=max_q, window=window)
+    _operand(lse, "lse", torch.float32, 2, device)
+    if lse.shape != (n, q_heads) or not lse.is_contiguous():
+        raise ValueError("lse: a contiguous [n, q_heads] tensor is expected")
+    ld_out = _by_token(out, "out", torch.float32, heads, device)
+    ld_w = _by_token(weights, "weights", torch.float32, heads, device) if weights is not None else 0
+    tokens = k_cache.rows // heads if heads > 0 else 0
+    if out.shape[1] != tokens or (weights is not None and weights.shape[1] != tokens):
+        raise ValueError("out, weights: a column per token of the cache is expected")
+    lib = _lib.load()
+    if ws is not None:
+        _operand(ws, "ws", torch.uint8, 1, device)
+    else:
+        need = lib.nvfp4_workspace_size(_lib.OP_KV_WEIGHTS, n, q_heads, heads, D, seqs)
+        ws = _workspace(need, device) if need else None
+    kc = k_cache.c()
+    with _on(device):
+        st = lib.nvfp4_kv_weights(
+            _ptr(q), ld_q, n, q_heads, _ptr(lse), ctypes.byref(kc), heads, _ptr(block_table), ld_table, pages, page_size,
+            _ptr(kv_lens), _ptr(cu_q), seqs, max_q, D ** -0.5 if scale is None else scale, int(causal), window,
+            _ptr(weights), ld_w, _ptr(out), ld_out, _ptr(ws), 0 if ws is None else ws.numel(), _stream(device))
+    _check(st, "nvfp4_kv_weights")
+    return out
+
+
+def nvfp4_kv_select(weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int, keep: int,
+                    positions: torch.Tensor | None = None, next_positions: torch.Tensor | None = None, sinks: int = 0,
+                    recent: int = 0, cap: int | None = None):
+    """(moves, lens): the moves (int32 [seqs, heads, cap, 2], pairs of places, -1
+    behind the last) after which each KV head of a sequence of more than `keep`
+    tokens has the tokens that it keeps at its first `keep` places, and the lengths
+    afterwards (int32 [seqs]).  Kept are the tokens at positions below sinks, the
+    `recent` ones before next_positions (int32 [seqs]) and the heaviest of
+    weights (float32 [heads, cache tokens]).  positions: int32, the shape of
+    weights; None: places are positions.  cap: the most moves of a list (what the
+    table's width can need if omitted)."""
+    device = weights.device
+    seqs, pages, ld_table = _pages(block_table, kv_lens, device)
+    heads, tokens = weights.shape if weights.dim() == 2 else (0, 0)
+    ld_w = _by_token(weights, "weights", torch.float32, heads, device)
+    ld_p = 0
+    if positions is not None:
+        ld_p = _by_token(positions, "positions", torch.int32, heads, device)
+        if positions.shape != weights.shape or next_positions is None:
+            raise ValueError("positions: the shape of weights is expected, and next_positions")
+        _operand(next_positions, "next_positions", torch.int32, 1, device)
+        if next_positions.numel() != seqs:
+            raise ValueError("next_positions: one per row of block_table")
+    if cap is None:
+        cap = max(0, min(keep, pages * page_size - keep))
+    _int32(page_size=page_size, keep=keep, sinks=sinks, recent=recent, cap=cap)
+    if cap < 0:
+        raise ValueError(f"cap: {cap}")
+    moves = torch.empty((seqs, heads, cap, 2), dtype=torch.int32, device=device)
+    lens = torch.empty((seqs,), dtype=torch.int32, device=device)
+    with _on(device):
+        st = _lib.load().nvfp4_kv_select(
+            _ptr(weights), ld_w, _ptr(positions), ld_p, heads, tokens, _ptr(block_table), ld_table, pages, page_size,
+            _ptr(kv_lens), None if positions is None else _ptr(next_positions), seqs, keep, sinks, recent, _ptr(moves),
+            cap, _ptr(lens), _stream(device))
+    _check(st, "nvfp4_kv_select")
+    return moves, lens
+
+
+def nvfp4_kv_move(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, heads: int, block_table: torch.Tensor, page_size: int,
+                  moves: torch.Tensor, weights: torch.Tensor | None = None,
+                  positions: torch.Tensor | None = None) -> None:
+    """Carry out moves (int32 [seqs, heads or 1, cap, 2]: source and destination
+    places of each sequence, a negative source: none) of cached tokens: K and V,
+    and weights (float32) and positions (int32), [heads, cache tokens], where
+    given.  Of a list of at most 256 moves every source is read first."""
+    device = k_cache.device
+    _caches_on(device, k_cache, v_cache)
+    seqs, pages, ld_table = _pages(block_table, None, device)
+    _int32(heads=heads, page_size=page_size)
+    _operand(moves, "moves", torch.int32, 4, device)
+    if moves.shape[0] != seqs or moves.shape[3] != 2 or not moves.is_contiguous():
+        raise ValueError("moves: a contiguous [seqs, heads or 1, moves, 2] tensor is expected")
+    ld = [0, 0]
+    tokens = k_cache.rows // heads if heads > 0 else 0
+    for j, (name, t, dtype) in enumerate((("weights", weights, torch.float32), ("positions", positions, torch.int32))):
+        if t is not None:
+            ld[j] = _by_token(t, name, dtype, heads, device)
+            if t.shape[1] != tokens:
+                raise ValueError(f"{name}: a column per token of the cache is expected")
+    kc, vc = k_cache.c(), v_cache.c()
+    with _on(device):
+        st = _lib.load().nvfp4_kv_move(
+            ctypes.byref(kc), ctypes.byref(vc), heads, _ptr(block_table), ld_table, pages, page_size, seqs, _ptr(moves),
+            moves.shape[1], moves.shape[2], _ptr(weights), ld[0], _ptr(positions), ld[1], _stream(device))
+    _check(st, "nvfp4_kv_move")
 
 
 def mxfp8_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor | None, eps: float = 1e-6,

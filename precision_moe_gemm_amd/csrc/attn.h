@@ -59,6 +59,9 @@ struct AttnArgs {
     int kv_heads, group;     // group: query heads per KV head
     double scale_log2;       // scale * log2(e)
     int causal, window;
+    const uint32_t* mask;    // trees of drafts: bit j % 32 of word j / 32 of a query row: it sees draft j
+    int64_t ld_mask;         // words
+    int mask_words;
     uint16_t* out;           // [n, heads, D], token stride ld_out
     int64_t ld_out;
     float* lse;              // [n, heads] or null
@@ -182,6 +185,83 @@ NVFP4_DEV void attn_limits(const AttnArgs& a, const AttnSeq& s, int i, int* star
     }
     *end = e < 0 ? 0 : e;
     *start = b;
+}
+
+// ---- trees of drafts (TREE): the m query tokens of a sequence are its last m
+// tokens, as otherwise.  Each sees every token before them, [0, base), and of
+// the m themselves those of its mask; with a window, the last `window` of what
+// it sees.
+
+NVFP4_DEV int attn_tree_base(const AttnSeq& s) { return s.kv > s.nq ? s.kv - s.nq : 0; }
+
+// Drafts past the mask's words are seen by no row.
+NVFP4_DEV void attn_tree_check(const AttnArgs& a, const AttnSeq& s)
+{
+    if (s.nq > 32 * (int64_t)a.mask_words)
+        raise_error(NVFP4_ERR_RANGE);
+}
+
+// The mask of 32 tokens of which the first is draft j0 (tokens before the
+// drafts are seen), for the query token in row `row` of q.
+NVFP4_DEV uint32_t attn_tree_bits(const AttnArgs& a, int row, int j0)
+{
+    if (j0 <= -32)
+        return ~0u;
+    const uint32_t* m = a.mask + row * a.ld_mask;
+    const int w = j0 >> 5, sh = j0 & 31;  // (j0 < 0: word -1 is all ones)
+    const uint32_t lo = w < 0 ? ~0u : (w < a.mask_words ? m[w] : 0u);
+    const uint32_t hi = w + 1 < a.mask_words ? m[w + 1] : 0u;
+    return (uint32_t)((((uint64_t)hi << 32) | lo) >> sh);
+}
+
+// The first token that query token i (row `row` of q) sees under the window.
+NVFP4_DEV int attn_tree_start(const AttnArgs& a, const AttnSeq& s, int i)
+{
+    if (a.window <= 0)
+        return 0;
+    const uint32_t* m = a.mask + (int64_t)(s.q0 + i) * a.ld_mask;
+    const int base = s.kv - s.nq;  // (below zero: the first drafts are not cached)
+    const int first = base < 0 ? -base : 0;
+    int left = a.window;
+    const int words = (s.nq + 31) / 32 < a.mask_words ? (s.nq + 31) / 32 : a.mask_words;
+    for (int w = words - 1; w >= 0 && 32 * w + 31 >= first; w--) {
+        uint32_t bits = m[w];
+        if (32 * w + 32 > s.nq)
+            bits &= ~0u >> (32 * w + 32 - s.nq);
+        if (32 * w < first)
+            bits &= ~0u << (first - 32 * w);
+        const int c = __builtin_popcount(bits);
+        if (c >= left) {
+            while (--left > 0)
+                bits &= ~(0x80000000u >> __builtin_clz(bits));
+            return base + 32 * w + 31 - __builtin_clz(bits);
+        }
+        left -= c;
+    }
+    return base > left ? base - left : 0;
+}
+
+// The tokens [lo0, hi0) of the first and [lo1, hi1) of the last of the query
+// tokens i0 .. i1.  TREE: every row sees tokens of [lo0, hi1) only, and all of
+// [lo1, hi0).
+template <bool TREE>
+NVFP4_DEV void attn_span(const AttnArgs& a, const AttnSeq& s, int i0, int i1, int* lo0, int* hi0, int* lo1, int* hi1)
+{
+    if constexpr (TREE) {
+        const int base = attn_tree_base(s);
+        *lo0 = *lo1 = 0;
+        if (a.window > 0) {
+            // (a row of no draft sees `window` tokens before them, a row of all of them fewer by their number)
+            const int from = base - a.window, most = from + s.nq;
+            *lo0 = from > 0 ? from : 0;
+            *lo1 = most < 0 ? 0 : (most < base ? most : base);
+        }
+        *hi0 = base;
+        *hi1 = s.kv;
+    } else {
+        attn_limits(a, s, i0, lo0, hi0);
+        attn_limits(a, s, i1, lo1, hi1);
+    }
 }
 
 // Sequence b, uniform.  own: lane l's sequence l, where there are at most 64.
@@ -369,13 +449,14 @@ struct AttnPages {
 };
 
 // A wave's walk over the tokens of one KV head for 16 NT query rows.
-template <int D, int NT>
+template <int D, int NT, bool TREE = false>
 struct AttnWave {
     half8_t q[NT][D / 32];
     float4_t o[NT][D / 16];
     float m[NT], l[NT], c1[NT];
     int k[NT];  // m, c1 and the scores are in units of 2^k
     int start[NT], end[NT];
+    int token[TREE ? NT : 1], base;  // TREE: the rows' query tokens (rows of q and of the mask); the first draft
     // the lane's part of the copies: its place in 16 tokens' codes (of the even and the odd copies of a
     // half) and its row among the 32 tokens' scales
     uint32_t co[2], so;
@@ -385,6 +466,7 @@ struct AttnWave {
     {
         const float kg = *a.k_global;
         const uint32_t lane = threadIdx.x & 63, stride = a.kv_heads;
+        base = s.kv - s.nq;
         const uint32_t r = (lane / (D / 32)) & 15, c = lane % (D / 32);
         co[0] = r * stride * (D / 2) + 16 * (c ^ attn_swz<D>(r));
         co[1] = D == 256 ? (r + 8) * stride * (D / 2) + 16 * (c ^ attn_swz<D>(r + 8)) : co[0];
@@ -397,8 +479,15 @@ struct AttnWave {
             start[t] = end[t] = 0;
             u32x4 w[D / 32];
             uint32_t am = 0;
-            if (in)
+            if constexpr (TREE) {
+                token[t] = s.q0 + (in ? i : 0);
+                if (in) {
+                    start[t] = attn_tree_start(a, s, i);
+                    end[t] = s.kv;
+                }
+            } else if (in) {
                 attn_limits(a, s, i, &start[t], &end[t]);
+            }
             const uint16_t* src = a.q + (int64_t)(s.q0 + (in ? i : 0)) * a.ld_q + (int64_t)(h * a.group + hh) * D +
                                   lane_g() * (D / 4);
 #pragma unroll
@@ -457,7 +546,9 @@ struct AttnWave {
             __builtin_amdgcn_global_load_lds((const void*)src, (attn_lds_t)(dst + 16 * D), 4, 0, 0);
     }
 
-    // S^T of one step: tokens t0 .. t0 + 32 from a finished copy of K
+    // S^T of one step: tokens t0 .. t0 + 32 from a finished copy of K (SWAP: S, the rows of q as rows and the
+    // tokens as columns)
+    template <bool SWAP = false>
     NVFP4_DEV void scores(const uint8_t* src, float4_t (&s)[NT][2]) const
     {
         const int n = lane_n(), g = lane_g();
@@ -498,23 +589,28 @@ struct AttnWave {
                 const half8_t k = decode_row8(kc[half][c], scale_pair(b, b));
 #pragma unroll
                 for (int t = 0; t < NT; t++)
-                    s[t][half] = mfma16(k, q[t][c], s[t][half]);
+                    s[t][half] = SWAP ? mfma16(q[t][c], k, s[t][half]) : mfma16(k, q[t][c], s[t][half]);
             }
         }
     }
 
     // P^T of one step; ok: which halves lie in a page of the cache
-    NVFP4_DEV void weights(float4_t (&s)[NT][2], half8_t (&p)[NT], int t0, bool inside, const bool (&ok)[2])
+    NVFP4_DEV void weights(const AttnArgs& a, float4_t (&s)[NT][2], half8_t (&p)[NT], int t0, bool inside,
+                           const bool (&ok)[2])
     {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             if (!inside) {
+                uint32_t bits = 0;
+                if constexpr (TREE)
+                    bits = attn_tree_bits(a, token[t], t0 - base) >> lane_g();
 #pragma unroll
                 for (int half = 0; half < 2; half++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const int tok = t0 + 16 * half + 4 * i + lane_g();
-                        const bool seen = ok[half] && tok >= start[t] && tok < end[t];
+                        const bool seen = ok[half] && tok >= start[t] && tok < end[t] &&
+                                          (!TREE || (bits >> (16 * half + 4 * i) & 1));
                         s[t][half][i] = seen ? s[t][half][i] : -__builtin_inff();
                     }
             }
@@ -647,7 +743,7 @@ struct AttnWave {
             scores(bufk, s);
             rows(a, pages, row, next, h);
             request(a.k_packed, a.k_scales, row, bufk);
-            weights(s, p, t, ok[0] && ok[1] && t >= lo && t + kAttnStep <= hi, ok);
+            weights(a, s, p, t, ok[0] && ok[1] && t >= lo && t + kAttnStep <= hi, ok);
             wait_copies<kCopies>();
             values(bufv, p);
             request(a.v_packed, a.v_scales, row, bufv);
@@ -673,8 +769,8 @@ struct AttnWave {
 // holds head lane w % hl and token lane w / hl.  buf: D / 4 + 2 floats x 64
 // lanes x NT per writing wave, half the waves at most.  Afterwards token lane
 // 0 holds the whole.
-template <int D, int NT>
-NVFP4_DEV void attn_join(AttnWave<D, NT>& w, int hl, int wave, float* buf)
+template <int D, int NT, bool TREE>
+NVFP4_DEV void attn_join(AttnWave<D, NT, TREE>& w, int hl, int wave, float* buf)
 {
     constexpr int kRow = D / 4 + 2;
     const int tl = wave / hl, lane = threadIdx.x & 63;
@@ -709,8 +805,8 @@ NVFP4_DEV void attn_join(AttnWave<D, NT>& w, int hl, int wave, float* buf)
 }
 
 // Rows of a finished wave: o V-global / l as bf16, and lse.
-template <int D, int NT>
-NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT>& w, const AttnSeq& s, int h, int row0)
+template <int D, int NT, bool TREE>
+NVFP4_DEV void attn_finish(const AttnArgs& a, const AttnWave<D, NT, TREE>& w, const AttnSeq& s, int h, int row0)
 {
     const float vg = *a.v_global;
 #pragma unroll
@@ -755,12 +851,11 @@ NVFP4_DEV int attn_shares(const AttnArgs& a, int total)
     return most < a.workers ? most : a.workers;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 NVFP4_DEV AttnCount attn_count(const AttnArgs& a, const AttnSeq& s)
 {
     int lo0, hi0, lo1, hi1;
-    attn_limits(a, s, 0, &lo0, &hi0);
-    attn_limits(a, s, s.nq > 0 ? s.nq - 1 : 0, &lo1, &hi1);
+    attn_span<TREE>(a, s, 0, s.nq > 0 ? s.nq - 1 : 0, &lo0, &hi0, &lo1, &hi1);
     const int t0 = lo0 & ~(kAttnStep - 1);
     AttnCount c;
     c.tiles = (s.nq * a.group + 16 * NT - 1) / (16 * NT);
@@ -784,7 +879,7 @@ struct AttnTile {
 // the tile's first unit, else in slot 0 (a share has at most one of each).
 // A workgroup holds head_lanes KV heads side by side, which lie next to each
 // other in memory, and (waves / head_lanes) runs of the tokens.
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__((64 * attn_waves<D, NT>()), (D * NT <= 64 ? 4 : (D * NT <= 256 ? 2 : 1)))
 attn_rows_kernel(AttnArgs a)
 {
@@ -803,7 +898,7 @@ attn_rows_kernel(AttnArgs a)
     AttnSeq own{0, 0, 0, false};
     auto count = [&](int b) {
         own = attn_seq(a, b);
-        AttnCount c = attn_count<D, NT>(a, own);
+        AttnCount c = attn_count<D, NT, TREE>(a, own);
         c.units = a.whole ? 1 : c.units;  // whole tiles: w counts tiles
         return c;
     };
@@ -818,7 +913,7 @@ attn_rows_kernel(AttnArgs a)
     AttnFound f = attn_find(scan, a.seqs, u, count);
     while (u < u1) {
         const AttnSeq s = attn_seq_uniform(a, own, f.seq);
-        AttnCount c = attn_count<D, NT>(a, s);
+        AttnCount c = attn_count<D, NT, TREE>(a, s);
         const int units = c.units;
         c.units = a.whole ? 1 : c.units;
         if (f.at >= c.tiles * c.units) {
@@ -837,10 +932,14 @@ attn_rows_kernel(AttnArgs a)
         }
         int any, none, lo0, hi0, lo1, hi1;  // tokens of the sequence's, the tile's first and last row
         const int last = (row0 + 16 * NT - 1) / a.group;
-        attn_limits(a, s, 0, &any, &none);
-        attn_limits(a, s, row0 / a.group, &lo0, &hi0);
-        attn_limits(a, s, last < s.nq ? last : s.nq - 1, &lo1, &hi1);
-        AttnWave<D, NT> x;
+        attn_span<TREE>(a, s, row0 / a.group, last < s.nq ? last : s.nq - 1, &lo0, &hi0, &lo1, &hi1);
+        if constexpr (TREE) {
+            any = lo0;
+            attn_tree_check(a, s);
+        } else {
+            attn_limits(a, s, 0, &any, &none);
+        }
+        AttnWave<D, NT, TREE> x;
         x.open(a, s, h, row0);
         const int t0 = (any & ~(kAttnStep - 1)) + first * kAttnStep;
         const int share = (n + tls - 1) / tls * kAttnStep;
@@ -852,12 +951,12 @@ attn_rows_kernel(AttnArgs a)
                bufk + wave * attn_stage<D>(), bufv + wave * attn_stage<D>());
         x.close();
         if (tls > 1) {
-            attn_join<D, NT>(x, hl, wave, (float*)bufk);
+            attn_join(x, hl, wave, (float*)bufk);
             __syncthreads();
         }
         if (tl == 0) {
             if (n == units) {
-                attn_finish<D, NT>(a, x, s, h, row0);
+                attn_finish(a, x, s, h, row0);
             } else {
                 const int slot = first == 0;
                 float* dst = a.partial + (((int64_t)w * blocks + hb) * 2 + slot) * hl * attn_part<D, NT>() +
@@ -1074,7 +1173,7 @@ NVFP4_DEV void scale_acc(float16_t (&o)[N], float f)
         }
 }
 
-template <int D, int NW>
+template <int D, int NW, bool TREE>
 __global__ void __launch_bounds__((64 * NW), (D == 256 ? 1 : 2))
 attn_tile_kernel(AttnArgs a)
 {
@@ -1116,8 +1215,9 @@ attn_tile_kernel(AttnArgs a)
     const int row0 = f.at * ROWS;
     int lo0, hi0, lo1, hi1;  // tokens of the tile's first and last row
     const int last = (row0 + ROWS - 1) / a.group;
-    attn_limits(a, s, row0 / a.group, &lo0, &hi0);
-    attn_limits(a, s, last < s.nq ? last : s.nq - 1, &lo1, &hi1);
+    attn_span<TREE>(a, s, row0 / a.group, last < s.nq ? last : s.nq - 1, &lo0, &hi0, &lo1, &hi1);
+    if constexpr (TREE)
+        attn_tree_check(a, s);
     // ---- this split's blocks [b0, b1) of the tile's
     int b0 = lo0 / kTileTok, b1 = hi1 > lo0 ? (hi1 + kTileTok - 1) / kTileTok : b0;
     if (gridDim.y > 1) {
@@ -1131,8 +1231,14 @@ attn_tile_kernel(AttnArgs a)
     const int qi = r / a.group, hh = r - qi * a.group;
     const bool in = qi < s.nq;
     int start = 0, end = 0;
-    if (in)
+    if constexpr (TREE) {
+        if (in) {
+            start = attn_tree_start(a, s, qi);
+            end = s.kv;
+        }
+    } else if (in) {
         attn_limits(a, s, qi, &start, &end);
+    }
     // (D = 256: converted behind the first requests of K and V, 2218 against 2257 us for 2048 rows on 30720
     // tokens; at D = 128 registers then spill and 4096 rows take 167 instead of 150)
     u32x4 qw[D / 16];
@@ -1324,13 +1430,18 @@ attn_tile_kernel(AttnArgs a)
         const int t0 = blk * kTileTok;
         if (!(t0 >= lo1 && t0 + kTileTok <= hi0 && (ok.x & ok.y & ok.z & ok.w) != 0)) {
 #pragma unroll
-            for (int p = 0; p < 2; p++)
+            for (int p = 0; p < 2; p++) {
+                uint32_t bits = 0;
+                if constexpr (TREE)
+                    bits = attn_tree_bits(a, s.q0 + (in ? qi : 0), t0 + 32 * p - (s.kv - s.nq)) >> (4 * e);
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const int tok = t0 + 32 * p + 8 * (i >> 2) + 4 * e + (i & 3);
-                    const bool seen = tok >= start && tok < end && ok[2 * p + (i >> 3)] != 0;
+                    const bool seen = tok >= start && tok < end && ok[2 * p + (i >> 3)] != 0 &&
+                                      (!TREE || (bits >> (8 * (i >> 2) + (i & 3)) & 1));
                     sc[p][i] = seen ? sc[p][i] : -__builtin_inff();
                 }
+            }
         }
         float top = sc[0][0];
 #pragma unroll

@@ -11,6 +11,7 @@
 
 #include "attn.h"
 #include "common.h"
+#include "evict.h"
 #include "gemm.h"
 #include "kvcache.h"
 #include "moe.h"
@@ -18,6 +19,7 @@
 #include "mx8.h"
 #include "norm.h"
 #include "quant.h"
+#include "weigh.h"
 
 #ifndef NVFP4_BUILD_STAMP
 #define NVFP4_BUILD_STAMP "unstamped"
@@ -89,16 +91,17 @@ nvfp4_status check_tensor(const nvfp4_tensor* t, bool need_global = true, bool t
     return NVFP4_OK;
 }
 
-// Whether two bf16 matrices of `rows` rows (wa and wb elements each, at strides
-// lda >= wa and ldb >= wb) share an element: side by side in one wider buffer
-// they do not.
-bool rows_share(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows)
+// Whether two matrices of `rows` rows (wa and wb elements of `size` bytes each, at
+// strides lda >= wa and ldb >= wb) share an element: side by side in one wider
+// buffer they do not.
+bool rows_share(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows,
+                int size = 2)
 {
     if (!a || !b || rows < 1)
         return false;
     if ((uintptr_t)a > (uintptr_t)b)
-        return rows_share(b, ldb, wb, a, lda, wa, rows);
-    const __int128 la = (__int128)lda * 2, lb = (__int128)ldb * 2, ea = wa * 2, eb = wb * 2;  // bytes
+        return rows_share(b, ldb, wb, a, lda, wa, rows, size);
+    const __int128 la = (__int128)lda * size, lb = (__int128)ldb * size, ea = wa * size, eb = wb * size;  // bytes
     __int128 at = (uintptr_t)b - (uintptr_t)a;  // a row of b, from a's first
     // with one stride the rows of b meet those of a as b's first does, only fewer of them
     for (int64_t j = 0; j < (la == lb ? 1 : rows) && at < (rows - 1) * la + ea; j++, at += lb) {
@@ -110,9 +113,10 @@ bool rows_share(const void* a, int64_t lda, int64_t wa, const void* b, int64_t l
 }
 
 // The same of an output that may also be the input itself, row for row.
-bool rows_clash(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t width, int64_t rows)
+bool rows_clash(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t width, int64_t rows,
+                int size = 2)
 {
-    return !(out == in && (ld_out == ld_in || rows <= 1)) && rows_share(out, ld_out, width, in, ld_in, width, rows);
+    return !(out == in && (ld_out == ld_in || rows <= 1)) && rows_share(out, ld_out, width, in, ld_in, width, rows, size);
 }
 
 // ---------------------------------------------------------------- checks
@@ -304,19 +308,19 @@ constexpr int64_t kWholeTiles = 256, kWholeTokens = 1024;
 // heads of 128: 22 us together with the shares (24 with 8192 waves, 23 with
 // 16384); 8 sequences, 4 heads of 256: 32, 32, 35; 64 sequences: 70, 70, 72.
 constexpr int64_t kJoinWaves = 4096;
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
 {
     const int64_t tiles = attention_tiles(a, 16 * NT);
     if (tiles * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens) {
         a.whole = 1;
         a.head_lanes = 1;
-        attn_rows_kernel<D, NT>
+        attn_rows_kernel<D, NT, TREE>
             <<<(unsigned)(ceil_div(tiles, 8) * 8 * a.kv_heads), 64 * attn_waves<D, NT>(), 0, st>>>(a);
         return launch_status();
     }
     const int blocks = a.kv_heads / a.head_lanes;
-    attn_rows_kernel<D, NT><<<(unsigned)(a.workers * blocks), 64 * attn_waves<D, NT>(), 0, st>>>(a);
+    attn_rows_kernel<D, NT, TREE><<<(unsigned)(a.workers * blocks), 64 * attn_waves<D, NT>(), 0, st>>>(a);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK)
         return s;
@@ -332,7 +336,7 @@ nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
     return launch_status();
 }
 
-template <int D, int NW>
+template <int D, int NW, bool TREE>
 nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
 {
     constexpr int ROWS = 32 * NW;
@@ -341,7 +345,7 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
         return NVFP4_ERR_UNSUPPORTED;
     const int64_t splits = std::min(attention_tile_splits(tiles, a.kv_heads),
                                     std::max<int64_t>(1, (int64_t)a.pages * a.page / (4 * kTileTok)));
-    attn_tile_kernel<D, NW><<<dim3((unsigned)(tiles * a.kv_heads), (unsigned)splits), 64 * NW, 0, st>>>(a);
+    attn_tile_kernel<D, NW, TREE><<<dim3((unsigned)(tiles * a.kv_heads), (unsigned)splits), 64 * NW, 0, st>>>(a);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK || splits == 1)
         return s;
@@ -349,26 +353,124 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
     return launch_status();
 }
 
-template <int D>
+template <int D, bool TREE>
 nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
 {
     a.head_lanes = attention_head_lanes(a.kv_heads);
     a.workers = attention_workers(a.kv_heads, a.head_lanes);
     if (max_q * a.group <= 16 && attention_rows_fit(a, 16))
-        return launch_attention_rows<D, 1>(a, st);
+        return launch_attention_rows<D, 1, TREE>(a, st);
     // (rows of a sequence and KV head, GPU time of row tiles of 32 and of tiles of 128 rows, 8 KV heads of 128,
     // 4000 tokens: 64 rows of 8 sequences 34 and 74 us, of 64 sequences 126 and 235; 128 rows of 64 sequences 245
     // and 239; one sequence 20 and 20.  With 32 KV heads and 64 prompts of 60 tokens 57 and 73, of 120 122 and
     // 112, 100 rows on 600 tokens of heads of 64 151 and 99.  Tiles of 16 rows for 32: 107 us where one of 32
     // takes 80, 64 sequences)
     if (max_q * a.group <= 64 && attention_rows_fit(a, 32))
-        return launch_attention_rows<D, 2>(a, st);
+        return launch_attention_rows<D, 2, TREE>(a, st);
     // (128 rows of 64 sequences, 128-row tiles and 256-row ones: 239 and 257 us, heads of 64 72 and 85; 192 rows
     // 391 and 283, 107 and 89)
     if (D == 256 || max_q * a.group <= 128)
-        return launch_attention_tiles<D, 4>(a, st);
+        return launch_attention_tiles<D, 4, TREE>(a, st);
     if constexpr (D < 256)
-        return launch_attention_tiles<D, 8>(a, st);
+        return launch_attention_tiles<D, 8, TREE>(a, st);
+}
+
+template <bool TREE>
+nvfp4_status launch_attention(const AttnArgs& a, int64_t D, int64_t max_q, hipStream_t st)
+{
+    return D == 64    ? launch_attention<64, TREE>(a, max_q, st)
+           : D == 128 ? launch_attention<128, TREE>(a, max_q, st)
+                      : launch_attention<256, TREE>(a, max_q, st);
+}
+
+// The sequences' pages.
+void set_pages(AttnArgs& a, const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq, int32_t page_size,
+               const int32_t* kv_lens, int32_t seqs, int64_t num_pages)
+{
+    a.kv_lens = kv_lens;
+    a.table = block_table;
+    a.ld_table = ld_table;
+    a.num_pages = num_pages;
+    a.seqs = seqs;
+    a.pages = pages_per_seq;
+    a.page = page_size;
+    // d = page / 8 in (2^s, 2^(s+1)], mul = ceil(2^(32+s) / d) < 2^32: n * mul >> (32 + s) is n / d for n < 2^31
+    const uint64_t d = page_size / 8;
+    a.page_shift = 0;
+    while ((2ull << a.page_shift) < d)
+        a.page_shift++;
+    a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
+}
+
+// ---------------------------------------------------------------- eviction
+// Query rows of a sequence and KV head up to which weights go by the row kernel.
+constexpr int64_t kWeighFew = 32;
+
+// The row kernel counts its steps in 31 bits; what does not fit goes to the
+// tile kernel.
+bool weights_rows_fit(const AttnArgs& a)
+{
+    return a.seqs * (ceil_div((int64_t)a.pages * a.page, kAttnStep) + 1) <= 0x7FFFFFFF;
+}
+
+size_t weights_ws_bytes(int64_t D) { return (size_t)kWeighJobs * (D == 256 ? 128 : 256) * sizeof(float); }
+
+template <int D, int NT>
+nvfp4_status launch_weights_rows(WeighArgs w, hipStream_t st)
+{
+    w.a.head_lanes = attention_head_lanes(w.a.kv_heads);
+    w.a.workers = attention_workers(w.a.kv_heads, w.a.head_lanes);
+    weigh_rows_kernel<D, NT><<<(unsigned)(w.a.workers * (w.a.kv_heads / w.a.head_lanes)), 512, 0, st>>>(w);
+    return launch_status();
+}
+
+template <int D>
+nvfp4_status launch_weights(const WeighArgs& w, int64_t max_q, hipStream_t st)
+{
+    const int64_t rows = max_q * w.a.group;
+    if (rows <= 16 && weights_rows_fit(w.a))
+        return launch_weights_rows<D, 1>(w, st);
+    if (rows <= kWeighFew && weights_rows_fit(w.a))
+        return launch_weights_rows<D, 2>(w, st);
+    // (units of all sequences, and one more each)
+    if (w.a.seqs * (ceil_div((int64_t)w.a.pages * w.a.page, weigh_block<D>()) + 1) * w.a.kv_heads > 0x7FFFFFFF)
+        return NVFP4_ERR_UNSUPPORTED;
+    weigh_tile_kernel<D><<<kWeighWorkers, 256, 0, st>>>(w);
+    nvfp4_status s = launch_status();
+    if (s != NVFP4_OK)
+        return s;
+    weigh_join_kernel<D><<<256, weigh_block<D>(), 0, st>>>(w);
+    return launch_status();
+}
+
+void launch_select(const SelectArgs& s, hipStream_t st)
+{
+    const unsigned grid = (unsigned)(s.a.seqs * s.a.kv_heads);
+    if ((int64_t)s.a.pages * s.a.page <= 4096)
+        select_kernel<4096><<<grid, kSelectThreads, 0, st>>>(s);
+    else
+        select_kernel<32768><<<grid, kSelectThreads, 0, st>>>(s);
+}
+
+void launch_move(const MoveArgs& m, hipStream_t st)
+{
+    const unsigned lists = (unsigned)(m.a.seqs * m.a.kv_heads);
+    if (m.cap <= kMoveTogether) {
+        int side = 1;
+        while (side < 64 && 64 / (2 * side) >= m.cap)
+            side *= 2;
+        const dim3 grid(lists, (unsigned)std::min<int64_t>(ceil_div(m.units, 4 * side), 64));
+        if (m.cap <= 64)
+            move_together_kernel<1><<<grid, 256, 0, st>>>(m, side);
+        else
+            move_together_kernel<4><<<grid, 256, 0, st>>>(m, 1);
+        return;
+    }
+    int lanes = 1;
+    while (lanes < 64 && lanes < m.units)
+        lanes *= 2;
+    move_apart_kernel<<<dim3(lists, (unsigned)std::min<int64_t>(ceil_div((int64_t)m.cap * lanes, 256), 8192)), 256, 0, st>>>(
+        m, lanes);
 }
 
 // RMS norm: a workgroup per row (up to 16 chunks of 8 elements per thread),
@@ -1163,6 +1265,10 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
             return 0;
         return attention_ws_bytes(T, k, E, H, I);
+    case NVFP4_OP_KV_WEIGHTS:
+        if (T <= 0 || H <= 0 || I <= 0)
+            return 0;
+        return weights_ws_bytes(H);
     }
     return 0;
 }
@@ -2262,16 +2368,24 @@ nvfp4_status nvfp4_kv_append(const void* q, int64_t ld_q, int32_t q_heads, const
     return launch_status();
 }
 
-nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
-                                const nvfp4_tensor* v_cache, int32_t kv_heads, const int32_t* block_table,
-                                int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
-                                const int32_t* cu_q, int32_t seqs, int32_t max_q, float scale, int32_t causal,
-                                int32_t window, void* out, int64_t ld_out, float* lse, void* ws, size_t ws_bytes,
-                                void* stream)
+// Attention over a paged cache; tree: the rows' masks, or null.
+struct TreeMask {
+    const uint32_t* bits;
+    int64_t ld;
+    int32_t words;
+};
+static nvfp4_status kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
+                                 const nvfp4_tensor* v_cache, int32_t kv_heads, const int32_t* block_table,
+                                 int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                                 const int32_t* cu_q, int32_t seqs, int32_t max_q, const TreeMask* tree, float scale,
+                                 int32_t causal, int32_t window, void* out, int64_t ld_out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream)
 {
     const nvfp4_tensor* cache[2] = {k_cache, v_cache};
     if (n < 0 || seqs < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || pages_per_seq < 0 ||
         ld_table < pages_per_seq || page_size < 1 || max_q < 0)
+        return NVFP4_ERR_SHAPE;
+    if (tree && (tree->words < 0 || tree->ld < tree->words))
         return NVFP4_ERR_SHAPE;
     for (int j = 0; j < 2; j++) {
         nvfp4_status s = check_tensor(cache[j]);
@@ -2299,6 +2413,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
         !aligned(lse, 4) || (pages_per_seq > 0 && !block_table) || !aligned(block_table, 4))
         return NVFP4_ERR_INVALID_ARG;
+    if (tree && ((tree->words > 0 && !tree->bits) || !aligned(tree->bits, 4)))
+        return NVFP4_ERR_INVALID_ARG;
     if (rows_share(q, ld_q, q_heads * D, out, ld_out, q_heads * D, n))
         return NVFP4_ERR_INVALID_ARG;
     // (a row's 16 scale bytes are one copy)
@@ -2319,19 +2435,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.k_global = k_cache->global;
     a.v_global = v_cache->global;
     a.cu_q = cu_q;
-    a.kv_lens = kv_lens;
-    a.table = block_table;
-    a.ld_table = ld_table;
-    a.num_pages = num_pages;
     a.n = n;
-    a.seqs = seqs;
-    a.pages = pages_per_seq;
-    a.page = page_size;
-    // d = page / 8 in (2^s, 2^(s+1)], mul = ceil(2^(32+s) / d) < 2^32: n * mul >> (32 + s) is n / d for n < 2^31
-    const uint64_t d = page_size / 8;
-    while ((2ull << a.page_shift) < d)
-        a.page_shift++;
-    a.page_mul = (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + d - 1) / d);
+    set_pages(a, block_table, ld_table, pages_per_seq, page_size, kv_lens, seqs, num_pages);
     a.kv_heads = kv_heads;
     a.group = q_heads / kv_heads;
     a.scale_log2 = (double)scale * 1.4426950408889634;
@@ -2344,9 +2449,12 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
     a.partial = (float*)((uint8_t*)ws + attention_tiles_bytes(n, a.group, seqs));
     if (!cu_q)
         max_q = 1;
-    nvfp4_status s = D == 64    ? launch_attention<64>(a, max_q, S(stream))
-                     : D == 128 ? launch_attention<128>(a, max_q, S(stream))
-                                : launch_attention<256>(a, max_q, S(stream));
+    if (tree) {
+        a.mask = tree->bits;
+        a.ld_mask = tree->ld;
+        a.mask_words = tree->words;
+    }
+    nvfp4_status s = tree ? launch_attention<true>(a, D, max_q, S(stream)) : launch_attention<false>(a, D, max_q, S(stream));
     if (s == NVFP4_OK && checks_on()) {
         // (pages that no sequence holds may be unwritten: no check of the scales)
         check_bf16(q, n, q_heads * D, ld_q, S(stream));
@@ -2355,6 +2463,213 @@ nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t 
         s = launch_status();
     }
     return s;
+}
+
+nvfp4_status nvfp4_kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
+                                const nvfp4_tensor* v_cache, int32_t kv_heads, const int32_t* block_table,
+                                int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                                const int32_t* cu_q, int32_t seqs, int32_t max_q, float scale, int32_t causal,
+                                int32_t window, void* out, int64_t ld_out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream)
+{
+    return kv_attention(q, ld_q, n, q_heads, k_cache, v_cache, kv_heads, block_table, ld_table, pages_per_seq, page_size,
+                        kv_lens, cu_q, seqs, max_q, nullptr, scale, causal, window, out, ld_out, lse, ws, ws_bytes, stream);
+}
+
+nvfp4_status nvfp4_kv_attention_tree(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const nvfp4_tensor* k_cache,
+                                     const nvfp4_tensor* v_cache, int32_t kv_heads, const int32_t* block_table,
+                                     int64_t ld_table, int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                                     const int32_t* cu_q, int32_t seqs, int32_t max_q, const uint32_t* mask,
+                                     int64_t ld_mask, int32_t mask_words, float scale, int32_t window, void* out,
+                                     int64_t ld_out, float* lse, void* ws, size_t ws_bytes, void* stream)
+{
+    const TreeMask tree{mask, ld_mask, mask_words};
+    return kv_attention(q, ld_q, n, q_heads, k_cache, v_cache, kv_heads, block_table, ld_table, pages_per_seq, page_size,
+                        kv_lens, cu_q, seqs, max_q, &tree, scale, 1, window, out, ld_out, lse, ws, ws_bytes, stream);
+}
+
+// A paged cache's sequences: sizes, then (with something to do) pointers and what this build takes.
+static nvfp4_status check_pages(int64_t tokens, int32_t kv_heads, const int32_t* block_table, int64_t ld_table,
+                                int32_t pages_per_seq, int32_t page_size, int32_t seqs)
+{
+    if (seqs < 0 || kv_heads < 1 || pages_per_seq < 0 || ld_table < pages_per_seq || page_size < 1 || tokens < 0)
+        return NVFP4_ERR_SHAPE;
+    if (seqs == 0)
+        return NVFP4_OK;
+    if (page_size % 16 != 0 || tokens > 0x7FFFFFFF || (int64_t)pages_per_seq * page_size > 0x40000000 || kv_heads > 65535 ||
+        (int64_t)seqs * kv_heads > 0x3FFFFF)
+        return NVFP4_ERR_UNSUPPORTED;
+    if (pages_per_seq > 0 && tokens < page_size)
+        return NVFP4_ERR_SHAPE;
+    if ((pages_per_seq > 0 && !block_table) || !aligned(block_table, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_kv_weights(const void* q, int64_t ld_q, int64_t n, int32_t q_heads, const float* lse,
+                              const nvfp4_tensor* k_cache, int32_t kv_heads, const int32_t* block_table, int64_t ld_table,
+                              int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens, const int32_t* cu_q,
+                              int32_t seqs, int32_t max_q, float scale, int32_t causal, int32_t window,
+                              const float* weights, int64_t ld_weights, float* weights_out, int64_t ld_out, void* ws,
+                              size_t ws_bytes, void* stream)
+{
+    if (n < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || max_q < 0)
+        return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_tensor(k_cache);
+    if (st != NVFP4_OK)
+        return st;
+    if (k_cache->batch != 1 || k_cache->rows % kv_heads != 0 || (!cu_q && n != seqs))
+        return NVFP4_ERR_SHAPE;
+    const int64_t D = k_cache->cols, tokens = k_cache->rows / kv_heads;
+    if (!(scale > 0.0f) || scale > 3.0e38f || window < 0 || (window > 0 && !causal))
+        return NVFP4_ERR_INVALID_ARG;
+    st = check_pages(tokens, kv_heads, block_table, ld_table, pages_per_seq, page_size, seqs);
+    if (st != NVFP4_OK)
+        return st;
+    if (seqs == 0 || pages_per_seq == 0)
+        return NVFP4_OK;
+    if ((D != 64 && D != 128 && D != 256) || n > 0x7FFFFF00 || n * q_heads > 0x7FFFFF00)
+        return NVFP4_ERR_UNSUPPORTED;
+    if (ld_q < q_heads * D || ld_q % 8 != 0 || (weights && ld_weights < tokens) || ld_out < tokens)
+        return NVFP4_ERR_SHAPE;
+    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
+        !aligned(weights, 4) || !weights_out || !aligned(weights_out, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows_clash(weights_out, ld_out, weights, ld_weights, tokens, kv_heads, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    if (D == 256 && !aligned(k_cache->scales, 16))
+        return NVFP4_ERR_INVALID_ARG;
+    const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs);
+    if (need > 0 && (!ws || !aligned(ws, 256)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < need)
+        return NVFP4_ERR_WORKSPACE;
+    WeighArgs w{};
+    w.a.q = (const uint16_t*)q;
+    w.a.ld_q = ld_q;
+    w.a.k_packed = k_cache->packed;
+    w.a.k_scales = k_cache->scales;
+    w.a.k_global = k_cache->global;
+    w.a.cu_q = cu_q;
+    w.a.n = n;
+    set_pages(w.a, block_table, ld_table, pages_per_seq, page_size, kv_lens, seqs, tokens / page_size);
+    w.a.kv_heads = kv_heads;
+    w.a.group = q_heads / kv_heads;
+    w.a.scale_log2 = (double)scale * 1.4426950408889634;
+    w.a.causal = causal != 0;
+    w.a.window = window;
+    w.lse = lse;
+    w.before = weights;
+    w.ld_before = ld_weights;
+    w.after = weights_out;
+    w.ld_after = ld_out;
+    w.partial = (float*)ws;
+    if (!cu_q)
+        max_q = 1;
+    st = D == 64    ? launch_weights<64>(w, max_q, S(stream))
+         : D == 128 ? launch_weights<128>(w, max_q, S(stream))
+                    : launch_weights<256>(w, max_q, S(stream));
+    if (st == NVFP4_OK && checks_on()) {
+        check_bf16(q, n, q_heads * D, ld_q, S(stream));
+        check_globals(k_cache->global, 1, S(stream));
+        st = launch_status();
+    }
+    return st;
+}
+
+nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int32_t* positions, int64_t ld_positions,
+                             int32_t kv_heads, int64_t tokens, const int32_t* block_table, int64_t ld_table,
+                             int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
+                             const int32_t* next_positions, int32_t seqs, int32_t keep, int32_t sinks, int32_t recent,
+                             int32_t* moves, int32_t cap, int32_t* lens_out, void* stream)
+{
+    nvfp4_status st = check_pages(tokens, kv_heads, block_table, ld_table, pages_per_seq, page_size, seqs);
+    if (st != NVFP4_OK)
+        return st;
+    if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep)
+        return NVFP4_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)pages_per_seq * page_size;
+    if (cap < 0 || (seqs > 0 && cap < std::min<int64_t>(keep, most - keep)))
+        return NVFP4_ERR_SHAPE;
+    if (seqs == 0)
+        return NVFP4_OK;
+    if (ld_weights < tokens || (positions && ld_positions < tokens))
+        return NVFP4_ERR_SHAPE;
+    if (!weights || !aligned(weights, 4) || !aligned(positions, 4) || (positions && !next_positions) ||
+        !aligned(next_positions, 4) || !kv_lens || !aligned(kv_lens, 4) || (cap > 0 && !moves) || !aligned(moves, 4) ||
+        !lens_out || !aligned(lens_out, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    // (one KV head's workgroup writes a length that the others read)
+    if (rows_share(lens_out, seqs, seqs, kv_lens, seqs, seqs, 1, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    SelectArgs a{};
+    set_pages(a.a, block_table, ld_table, pages_per_seq, page_size, kv_lens, seqs, tokens / page_size);
+    a.a.kv_heads = kv_heads;
+    a.weights = weights;
+    a.ld_w = ld_weights;
+    a.positions = positions;
+    a.ld_pos = ld_positions;
+    a.next = next_positions;
+    a.keep = keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.moves = moves;
+    a.cap = cap;
+    a.lens = lens_out;
+    launch_select(a, S(stream));
+    return launch_status();
+}
+
+nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,
+                           const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq, int32_t page_size,
+                           int32_t seqs, const int32_t* moves, int32_t lists, int32_t cap, float* weights,
+                           int64_t ld_weights, int32_t* positions, int64_t ld_positions, void* stream)
+{
+    const nvfp4_tensor* cache[2] = {k_cache, v_cache};
+    if (kv_heads < 1 || (lists != 1 && lists != kv_heads) || cap < 0)
+        return NVFP4_ERR_SHAPE;
+    for (int j = 0; j < 2; j++) {
+        nvfp4_status s = check_tensor(cache[j], false);
+        if (s != NVFP4_OK)
+            return s;
+        if (cache[j]->batch != 1 || cache[j]->rows % kv_heads != 0)
+            return NVFP4_ERR_SHAPE;
+    }
+    const int64_t D = k_cache->cols, tokens = k_cache->rows / kv_heads;
+    if (v_cache->cols != D || v_cache->rows != k_cache->rows)
+        return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_pages(tokens, kv_heads, block_table, ld_table, pages_per_seq, page_size, seqs);
+    if (st != NVFP4_OK)
+        return st;
+    if (seqs == 0 || cap == 0 || pages_per_seq == 0)
+        return NVFP4_OK;
+    if (D == 0 || D % 32 != 0 || D > 4096)
+        return NVFP4_ERR_UNSUPPORTED;
+    if ((weights && ld_weights < tokens) || (positions && ld_positions < tokens))
+        return NVFP4_ERR_SHAPE;
+    if (!moves || !aligned(moves, 4) || !aligned(weights, 4) || !aligned(positions, 4))
+        return NVFP4_ERR_INVALID_ARG;
+    MoveArgs m{};
+    set_pages(m.a, block_table, ld_table, pages_per_seq, page_size, nullptr, seqs, tokens / page_size);
+    m.a.kv_heads = kv_heads;
+    for (int j = 0; j < 2; j++) {
+        m.codes[j] = cache[j]->packed;
+        m.scales[j] = cache[j]->scales;
+    }
+    m.dim = (int)D;
+    m.scale_unit = D % 256 == 0 ? 16 : (D % 128 == 0 ? 8 : (D % 64 == 0 ? 4 : 2));
+    m.code_units = (int)(D / 32);
+    m.scale_units = (int)(D / 16 / m.scale_unit);
+    m.units = 2 * (m.code_units + m.scale_units) + (weights != nullptr) + (positions != nullptr);
+    m.weights = weights;
+    m.ld_w = ld_weights;
+    m.positions = positions;
+    m.ld_pos = ld_positions;
+    m.moves = moves;
+    m.lists = lists;
+    m.cap = cap;
+    launch_move(m, S(stream));
+    return launch_status();
 }
 
 nvfp4_status mxfp8_add_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, const void* weight,
