@@ -404,7 +404,7 @@ void set_pages(AttnArgs& a, const int32_t* block_table, int64_t ld_table, int32_
 
 // ---------------------------------------------------------------- eviction
 // Query rows of a sequence and KV head up to which weights go by the row kernel.
-constexpr int64_t kWeighFew = 32;
+constexpr int64_t kWeighFew = 64;
 
 // The row kernel counts its steps in 31 bits; what does not fit goes to the
 // tile kernel.
@@ -419,7 +419,7 @@ template <int D, int NT>
 nvfp4_status launch_weights_rows(WeighArgs w, hipStream_t st)
 {
     w.a.head_lanes = attention_head_lanes(w.a.kv_heads);
-    w.a.workers = attention_workers(w.a.kv_heads, w.a.head_lanes);
+    w.a.workers = weigh_rows_per_cu<D, NT>() * attention_workers(w.a.kv_heads, w.a.head_lanes);
     weigh_rows_kernel<D, NT><<<(unsigned)(w.a.workers * (w.a.kv_heads / w.a.head_lanes)), 512, 0, st>>>(w);
     return launch_status();
 }
@@ -430,12 +430,14 @@ nvfp4_status launch_weights(const WeighArgs& w, int64_t max_q, hipStream_t st)
     const int64_t rows = max_q * w.a.group;
     if (rows <= 16 && weights_rows_fit(w.a))
         return launch_weights_rows<D, 1>(w, st);
-    if (rows <= kWeighFew && weights_rows_fit(w.a))
+    if (rows <= 32 && weights_rows_fit(w.a))
         return launch_weights_rows<D, 2>(w, st);
+    if (rows <= kWeighFew && weights_rows_fit(w.a))
+        return launch_weights_rows<D, 4>(w, st);
     // (units of all sequences, and one more each)
     if (w.a.seqs * (ceil_div((int64_t)w.a.pages * w.a.page, weigh_block<D>()) + 1) * w.a.kv_heads > 0x7FFFFFFF)
         return NVFP4_ERR_UNSUPPORTED;
-    weigh_tile_kernel<D><<<kWeighWorkers, 256, 0, st>>>(w);
+    weigh_tile_kernel<D><<<kWeighWorkers, 64 * weigh_waves<D>(), 0, st>>>(w);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK)
         return s;

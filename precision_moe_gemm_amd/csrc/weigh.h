@@ -15,7 +15,7 @@
 //
 // S = Q K^T with a token per column: a lane holds the scores of one token for
 // several rows, and the sum over the rows stays within the lane until the last
-// step.  Both products' operand layouts are those of attn.h.
+// step.
 #pragma once
 #include "attn.h"
 
@@ -38,6 +38,22 @@ NVFP4_DEV float weigh_exp(float x) { return __builtin_amdgcn_fmed3f(__builtin_am
 NVFP4_DEV float weigh_shift(float lse)
 {
     return __builtin_fabsf(lse) <= 3.402823466e38f ? lse * -1.4426950408889634f : -__builtin_inff();
+}
+
+// The shifts of the 16 rows 8 i + .. + 4 of a tile, from shared memory.  (The compiler would have reads of it wait
+// for all copies in flight, which go to other arrays, so they and their wait are written out.)
+NVFP4_DEV void weigh_shifts(const float* src, float4_t (&z)[4])
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) float*)src;
+    asm volatile(
+        "ds_read_b128 %0, %4\n\t"
+        "ds_read_b128 %1, %4 offset:32\n\t"
+        "ds_read_b128 %2, %4 offset:64\n\t"
+        "ds_read_b128 %3, %4 offset:96\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(z[0]), "=&v"(z[1]), "=&v"(z[2]), "=&v"(z[3])
+        : "v"(at)
+        : "memory");
 }
 
 // The tokens whose weights a call writes: all of a sequence's, without those
@@ -72,6 +88,12 @@ NVFP4_DEV void weigh_put(const WeighArgs& w, const int32_t* table_row, int h, in
 // runs of neighbours.
 // ---------------------------------------------------------------------------
 constexpr int kWeighRun = 512;
+
+// Workgroups of eight waves on a CU.  Two, where the registers of four waves on a SIMD hold the queries (64
+// sequences of 4000 tokens, 16 rows: 43.3 us; one: 52.3; three shares a CU for two places: 45.6).  One with more rows
+// (40 rows, 16 sequences of 8000: 50.2; two: 60.2) and with D = 256 (one sequence of 262144: 41.3; two: 49.2).
+template <int D, int NT>
+constexpr int weigh_rows_per_cu() { return D <= 128 && NT <= 2 ? 2 : 1; }
 
 template <int D, int NT>
 struct WeighRows {
@@ -158,17 +180,20 @@ struct WeighRows {
         };
         request(buf0);
         request(buf1);
-        for (int t = t0; t < t1; t += 2 * kAttnStep) {
+        // (no branch in the loop: with one the compiler waits for both copies before it reads the first)
+        int t = t0;
+        for (; t + kAttnStep < t1; t += 2 * kAttnStep) {
             use(buf0, t);
-            if (t + kAttnStep < t1)
-                use(buf1, t + kAttnStep);
+            use(buf1, t + kAttnStep);
         }
+        if (t < t1)
+            use(buf0, t);
         wait_vm<0>();
     }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(512, (2 * weigh_rows_per_cu<D, NT>()))
 weigh_rows_kernel(WeighArgs w)
 {
     constexpr int kWaves = 8;
@@ -247,28 +272,37 @@ weigh_rows_kernel(WeighArgs w)
 
 // ---------------------------------------------------------------------------
 // Many query rows per sequence: the time is the product and the exponentials.
-// A workgroup of four waves takes a block of tokens of one KV head, 64 per
-// wave (32 where D = 256), and walks the rows in tiles of 32.  K is decoded to
-// bf16 once (six significant bits: exact) and stays in registers; q goes to the
-// products as it is, copied into shared memory a tile ahead, so that no
-// element is converted in the loop.  Blocks and parts of their rows are jobs
-// of about equal size for two workgroups per CU; where rows are split, a second
-// launch adds the parts in their order.
+// A wave takes 32 tokens of one KV head, a workgroup the block of tokens of its
+// waves, and walks the rows in tiles of 32.  K is decoded to bf16 once (six
+// significant bits: exact) and stays in registers; q goes to the products as
+// it is, copied into shared memory three tiles ahead, so that no element is
+// converted in the loop.  Blocks and parts of their rows are jobs of about
+// equal size; where rows are split, a second launch adds the parts in their
+// order.
 //
 // v_mfma_f32_32x32x16_bf16 (A: row l % 32, B: column l % 32, both elements
 // 8 (l / 32) .. + 8 of the contraction; output: column l % 32, rows
 // 8 (i / 4) + 4 (l / 32) + i % 4).  The contraction's order is free: lane half
 // e takes elements [e D / 2, + D / 2).
+//
+// An element costs a multiply-add, an exponential (10 cycles of a wave) and an
+// addition on the vector unit and D / 512 cycles on the matrix unit.  A wave issues
+// a vector instruction about every seven cycles and no more, so up to D = 128
+// there are four waves on a SIMD, each with its products and then its
+// exponentials.  With D = 256, whose K alone takes 64 registers, there are two,
+// and a tile's exponentials stand between the products of the next.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 template <int D>
-constexpr int weigh_cols() { return D == 256 ? 1 : 2; }  // columns of 32 tokens per wave
+constexpr bool weigh_turns() { return D == 256; }
 template <int D>
-constexpr int weigh_block() { return 128 * weigh_cols<D>(); }  // tokens of a workgroup
-constexpr int kWeighRows = 2048;    // rows whose shifts are in shared memory at a time
+constexpr int weigh_waves() { return D == 256 ? 4 : 8; }
+template <int D>
+constexpr int weigh_block() { return 32 * weigh_waves<D>(); }  // tokens of a workgroup
+constexpr int kWeighRows = 1024;    // rows whose shifts are in shared memory at a time (a multiple of 128)
 constexpr int kWeighWorkers = 512;  // workgroups, two per CU
-constexpr int kWeighJobs = 2048;    // parts of split blocks, at most
+constexpr int kWeighJobs = 1024;    // parts of split blocks, at most
 
 // The blocks of tokens of a sequence.
 template <int D>
@@ -306,11 +340,12 @@ NVFP4_DEV void weigh_span(const AttnArgs& a, const AttnSeq& s, int t0, int t1, i
 }
 
 template <int D>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__((64 * weigh_waves<D>()), (weigh_turns<D>() ? 2 : 4))
 weigh_tile_kernel(WeighArgs w)
 {
-    constexpr int NC = weigh_cols<D>(), BT = weigh_block<D>(), N = D / 16, C = D / 8;  // C: chunks of a q row
-    __shared__ __attribute__((aligned(16))) u32x4 q0[32 * C], q1[32 * C];
+    constexpr int BT = weigh_block<D>(), NT = 64 * weigh_waves<D>(), N = D / 16, C = D / 8;  // C: chunks of a q row
+    // (separate arrays, picked at compile time, so that reads of one do not wait for the copies into another)
+    __shared__ __attribute__((aligned(16))) u32x4 q0[32 * C], q1[32 * C], q2[32 * C], q3[32 * C];
     __shared__ __attribute__((aligned(16))) float shift[kWeighRows];
     __shared__ __attribute__((aligned(16))) int limit[kWeighRows];  // a row sees the tokens below
     const AttnArgs& a = w.a;
@@ -330,8 +365,8 @@ weigh_tile_kernel(WeighArgs w)
     // Jobs in rounds of one per workgroup, every other round backwards: in a
     // causal sequence the first blocks have the most rows.
     for (int round = 0;; round++) {
-        const int turn = round & 1 ? (kWeighWorkers / 8 - 1 - (int)blockIdx.x / 8) * 8 + (int)blockIdx.x % 8 : (int)blockIdx.x;
-        const int64_t job = (int64_t)round * kWeighWorkers + turn;
+        const int place = round & 1 ? (kWeighWorkers / 8 - 1 - (int)blockIdx.x / 8) * 8 + (int)blockIdx.x % 8 : (int)blockIdx.x;
+        const int64_t job = (int64_t)round * kWeighWorkers + place;
         if ((int64_t)round * kWeighWorkers >= jobs)
             break;
         if (job >= jobs)
@@ -355,172 +390,226 @@ weigh_tile_kernel(WeighArgs w)
             r1 = r1 - r0 < per ? r1 : r0 + per;
         }
         // ---- K of this wave's tokens
-        const int tw = t0 + wave * 32 * NC;
-        bf16x8_t k[NC][N];
-#pragma unroll
-        for (int p = 0; p < NC; p++) {
-            const int t = tw + 32 * p + col;
-            const int i = attn_page(a, t < s.kv ? t : s.kv - 1);
+        const int tw = t0 + wave * 32, token = tw + col;
+        bf16x8_t k[N];
+        {
+            const int i = attn_page(a, token < s.kv ? token : s.kv - 1);
             const int page = table[i];
-            const bool ok = t < s.kv && page >= 0 && page < a.num_pages;
-            const int64_t row = ok ? ((int64_t)page * a.page + (t - i * a.page)) * a.kv_heads + h : h;
+            const bool ok = token < s.kv && page >= 0 && page < a.num_pages;
+            const int64_t row = ok ? ((int64_t)page * a.page + (token - i * a.page)) * a.kv_heads + h : h;
             uint32_t kc[D / 16], ks[D / 128 > 0 ? D / 128 : 1];
             load_bytes<D / 4>(a.k_packed + row * (D / 2) + e * (D / 4), kc);
             load_bytes<(D / 32 > 4 ? 4 : D / 32)>(a.k_scales + row * (D / 16) + e * (D / 32), ks);
             if constexpr (D == 256)
                 load_bytes<4>(a.k_scales + row * (D / 16) + e * (D / 32) + 4, ks + 1);
-#pragma unroll
-            for (int j = 0; j < N; j++) {
-                const uint32_t b = ks[j / 8] >> (8 * (j / 2 % 4));
-                const float sc = e4m3_decode(b & 0x7F);
-                const uint32_t x = kc[j];
+            for_range<0, N>([&](auto ji) ATTN_INLINE {
+                constexpr int j = decltype(ji)::value;
+                const float sc = e4m3_decode(ks[j / 8] >> (8 * (j / 2 % 4)) & 0x7F);
                 u32x4 v;
-#define WEIGH_PAIR(I)                                      \
-    {                                                      \
-        const float2_t y = __builtin_bit_cast(float2_t, FP4_TO_F32X2(x, I)); \
-        v[I] = pack_bf16x2(y.x * sc, y.y * sc);            \
-    }
-                WEIGH_PAIR(0)
-                WEIGH_PAIR(1)
-                WEIGH_PAIR(2)
-                WEIGH_PAIR(3)
-#undef WEIGH_PAIR
-                k[p][j] = __builtin_bit_cast(bf16x8_t, v);
-            }
+                for_range<0, 4>([&](auto ii) ATTN_INLINE {
+                    constexpr int i = decltype(ii)::value;
+                    const float2_t y = __builtin_bit_cast(float2_t, FP4_TO_F32X2(kc[j], i));
+                    v[i] = pack_bf16x2(y.x * sc, y.y * sc);
+                });
+                k[j] = __builtin_bit_cast(bf16x8_t, v);
+            });
         }
-        float sum[NC];
-#pragma unroll
-        for (int p = 0; p < NC; p++)
-            sum[p] = 0.0f;
+        float sum = 0.0f;
         // Copies of a tile: chunk ch of row rr goes to slot ch ^ swizzle of its row.  The tiles are copied in
         // order, so that a row's query token and head advance by 32 / group and 32 % group.
-        constexpr int NJ = 32 * C / 256;
-        int row[NJ], qi[NJ], hh[NJ];
+        constexpr int NJ = 32 * C > NT ? 32 * C / NT : 1;
+        const bool copies = 32 * C >= NT || wave * 64 < 32 * C;
+        const uint16_t* next[NJ];
+        int hh[NJ];
+        int next_row = r0;
+        auto chunk = [&](int j) ATTN_INLINE {
+            const int rr = (j * NT + tid) / C, ch = (j * NT + tid) % C;
+            return 8 * (ch ^ (C >= 16 ? rr & 15 : (rr >> 1) & 7));
+        };
+        auto row_at = [&](int row) ATTN_INLINE {
+            const int i = row / a.group;
+            return a.q + (int64_t)(s.q0 + i) * a.ld_q + (int64_t)(h * a.group + row - i * a.group) * D;
+        };
+        const int step_q = 32 / a.group, step_h = 32 - step_q * a.group;
+        const int64_t step = step_q * a.ld_q + step_h * D, wrap = a.ld_q - a.group * D;
 #pragma unroll
         for (int j = 0; j < NJ; j++) {
-            row[j] = r0 + (j * 256 + tid) / C;
-            qi[j] = row[j] / a.group;
-            hh[j] = row[j] - qi[j] * a.group;
+            const int row = r0 + (j * NT + tid) / C;
+            next[j] = row_at(row < r1 ? row : (r1 > 0 ? r1 - 1 : 0)) + chunk(j);
+            hh[j] = row % a.group;
         }
-        const int step_q = 32 / a.group, step_h = 32 - step_q * a.group;
-        const int last_q = r1 > 0 ? (r1 - 1) / a.group : 0, last_h = r1 > 0 ? r1 - 1 - last_q * a.group : 0;
         auto copy = [&](auto buf) ATTN_INLINE {
             constexpr int B = decltype(buf)::value;
+            const bool whole = next_row + 32 <= r1;  // (past the end the copies go on, so that their number is known)
+            if (copies) {
 #pragma unroll
-            for (int j = 0; j < NJ; j++) {
-                const int rr = (j * 256 + tid) / C, ch = (j * 256 + tid) % C;
-                const bool in = row[j] < r1;  // (past the end: the last row again)
-                const uint16_t* src = a.q + (int64_t)(s.q0 + (in ? qi[j] : last_q)) * a.ld_q +
-                                      (int64_t)(h * a.group + (in ? hh[j] : last_h)) * D +
-                                      8 * (ch ^ (C >= 16 ? rr & 15 : (rr >> 1) & 7));
-                __builtin_amdgcn_global_load_lds((const void*)src, (attn_lds_t)((B ? q1 : q0) + j * 256 + wave * 64), 16, 0,
-                                                 0);
-                row[j] += 32;
-                qi[j] += step_q;
-                hh[j] += step_h;
-                const bool over = hh[j] >= a.group;
-                hh[j] -= over ? a.group : 0;
-                qi[j] += over;
+                for (int j = 0; j < NJ; j++) {
+                    const uint16_t* src = next[j];
+                    if (!whole && next_row + (j * NT + tid) / C >= r1)  // past the end: the last row again
+                        src = row_at(r1 - 1) + chunk(j);
+                    u32x4* const dst = B == 0 ? q0 : (B == 1 ? q1 : (B == 2 ? q2 : q3));
+                    __builtin_amdgcn_global_load_lds((const void*)src, (attn_lds_t)(dst + j * NT + wave * 64), 16, 0, 0);
+                    next[j] += step;
+                    if (step_h != 0) {
+                        hh[j] += step_h;
+                        const bool over = hh[j] >= a.group;
+                        hh[j] -= over ? a.group : 0;
+                        next[j] += over ? wrap : 0;
+                    }
+                }
             }
+            next_row += 32;
         };
-        // weights of the tile of rows r .. r + 32
-        auto tile = [&](int r, int seg, int end, auto buf) ATTN_INLINE {
-            constexpr int B = decltype(buf)::value;
-            float16_t sc[NC];
-#pragma unroll
-            for (int p = 0; p < NC; p++)
+        int first_q = r0 / a.group, first_h = r0 - first_q * a.group;  // query token and head of the first row weighed next
+        float16_t s0, s1;
+        // One turn: the products of tile r (in buffer B) into `to`, and the weights of the tile before, whose
+        // products are in `from` (between the products, where both are asked for).
+        auto turn = [&](int r, int seg, auto buf, auto has_old, auto has_new, float16_t& from, float16_t& to) ATTN_INLINE {
+            constexpr int B = decltype(buf)::value, per = 16 / N;
+            const int old = r - 32;
+            float4_t z[4];
+            bool inside = true;
+            if constexpr (has_old) {
+                weigh_shifts(shift + (old - seg) + 4 * e, z);
+                // what the tile's first and last row see (rows behind the last one have no weight)
+                const int base = s.kv - s.nq, lo = base + first_q + 1, hi = base + first_q + (first_h + 31) / a.group + 1;
+                inside = tw + 32 <= s.kv && (!a.causal || (tw + 32 <= lo && (a.window <= 0 || tw >= hi - a.window)));
+                first_q += step_q;
+                first_h += step_h;
+                if (first_h >= a.group) {
+                    first_h -= a.group;
+                    first_q++;
+                }
+            }
+            if constexpr (has_new)
+                copy(std::integral_constant<int, (B + 3) % 4>{});
+            bf16x8_t f[N];
+            auto read = [&](auto ji) ATTN_INLINE {
+                constexpr int j = decltype(ji)::value;
+                const u32x4* const src = B == 0 ? q0 : (B == 1 ? q1 : (B == 2 ? q2 : q3));
+                f[j] = __builtin_bit_cast(bf16x8_t,
+                                          src[col * C + ((e * N + j) ^ (C >= 16 ? col & 15 : (col >> 1) & 7))]);
+            };
+            auto multiply = [&](auto ji) ATTN_INLINE {
+                constexpr int j = decltype(ji)::value;
+                if constexpr (j + 1 < N)
+                    read(std::integral_constant<int, j + 1>{});
+                to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[j], k[j], to, 0, 0, 0);
+            };
+            if constexpr (has_new) {
 #pragma unroll
                 for (int i = 0; i < 16; i++)
-                    sc[p][i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < N; j++) {
-                const int ch = e * N + j;
-                const bf16x8_t f = __builtin_bit_cast(
-                    bf16x8_t, (B ? q1 : q0)[col * C + (ch ^ (C >= 16 ? col & 15 : (col >> 1) & 7))]);
-#pragma unroll
-                for (int p = 0; p < NC; p++)
-                    sc[p] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, k[p][j], sc[p], 0, 0, 0);
+                    to[i] = 0.0f;
+                read(std::integral_constant<int, 0>{});
             }
-            float4_t z[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                z[i] = *(const float4_t*)(shift + (r - seg) + 8 * i + 4 * e);
-            // (rows behind the last one have no weight: any limits do)
-            const int lo = uniform(limit[r - seg]), hi = uniform(limit[(r + 31 < end ? r + 31 : end - 1) - seg]);
-            const bool inside = tw + 32 * NC <= lo && (a.window <= 0 || tw >= hi - a.window);
             if (inside) {
+                for_range<0, N>([&](auto ji) ATTN_INLINE {
+                    constexpr int j = decltype(ji)::value;
+                    if constexpr (has_new)
+                        multiply(ji);
+                    if constexpr (has_old)
 #pragma unroll
-                for (int p = 0; p < NC; p++) {
-                    float x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        x[i] = weigh_exp(__builtin_fmaf(sc[p][i], c, z[i >> 2][i & 3]));
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        sum[p] += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
-                }
+                        for (int i = j * per; i < (j + 1) * per; i++)
+                            sum += weigh_exp(__builtin_fmaf(from[i], c, z[i >> 2][i & 3]));
+                });
             } else {
+                if constexpr (has_new)
+                    for_range<0, N>(multiply);
+                if constexpr (has_old) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int to = limit[r - seg + 8 * (i >> 2) + 4 * e + (i & 3)];
-                    const int from = a.window > 0 ? to - a.window : 0;
-#pragma unroll
-                    for (int p = 0; p < NC; p++) {
-                        const int t = tw + 32 * p + col;
-                        const float x = weigh_exp(__builtin_fmaf(sc[p][i], c, z[i >> 2][i & 3]));
-                        sum[p] += t >= from && t < to ? x : 0.0f;
+                    for (int i = 0; i < 16; i++) {
+                        const int below = limit[old - seg + 8 * (i >> 2) + 4 * e + (i & 3)];
+                        const bool seen = token < below && (a.window <= 0 || token >= below - a.window);
+                        const float x = weigh_exp(__builtin_fmaf(from[i], c, z[i >> 2][i & 3]));
+                        sum += seen ? x : 0.0f;
                     }
                 }
             }
         };
         constexpr std::integral_constant<int, 0> zero{};
         constexpr std::integral_constant<int, 1> one{};
+        constexpr std::integral_constant<int, 2> two{};
+        constexpr std::integral_constant<int, 3> three{};
+        constexpr std::true_type yes{};
+        constexpr std::false_type no{};
+        // the next tile is here (of three on their way), and nobody reads the buffer of the last one any more
+        auto arrive = [&]() ATTN_INLINE {
+            wait_copies<2 * NJ>();
+            lds_barrier();
+        };
+        lds_barrier();  // nobody reads the last job's tiles any more
+        if (r0 < r1) {
+            copy(zero);
+            copy(one);
+            copy(two);
+        }
         for (int seg = r0; seg < r1; seg += kWeighRows) {
             const int end = r1 - seg < kWeighRows ? r1 : seg + kWeighRows;
-            __syncthreads();  // nobody reads the last rows' any more
-            copy(zero);
-            for (int x = tid; x < kWeighRows && x < ((end - seg + 31) & ~31); x += 256) {
+            lds_barrier();  // nobody reads the last rows' shifts any more
+            for (int x = tid; x < ((end - seg + 31) & ~31); x += NT) {
                 const int r = seg + x, i = r / a.group, head = h * a.group + r - i * a.group;
                 shift[x] = r < end ? weigh_shift(w.lse[(int64_t)(s.q0 + i) * (a.kv_heads * a.group) + head])
                                    : -__builtin_inff();
                 const int to = s.kv - s.nq + i + 1;
-                limit[x] = a.causal && to < s.kv ? to : s.kv;
+                limit[x] = !a.causal || to > s.kv ? s.kv : (to > 0 ? to : 0);
             }
-            for (int r = seg; r < end; r += 64) {
-                wait_vm<0>();
-                __syncthreads();
-                if (r + 32 < end)
-                    copy(one);
-                tile(r, seg, end, zero);
-                if (r + 32 >= end)
-                    break;
-                wait_vm<0>();
-                __syncthreads();
-                if (r + 64 < end)
-                    copy(zero);
-                tile(r + 32, seg, end, one);
+            const int tiles = (end - seg + 31) / 32;
+            // f(first row, buffer, parity) for tiles x0, x0 + 1, ... of the segment
+            auto each = [&](int x, auto f) ATTN_INLINE {
+                for (; x + 4 <= tiles; x += 4) {
+                    f(seg + 32 * x, one, one);
+                    f(seg + 32 * x + 32, two, zero);
+                    f(seg + 32 * x + 64, three, one);
+                    f(seg + 32 * x + 96, zero, zero);
+                }
+                if (x < tiles)
+                    f(seg + 32 * x, one, one);
+                if (x + 1 < tiles)
+                    f(seg + 32 * x + 32, two, zero);
+                if (x + 2 < tiles)
+                    f(seg + 32 * x + 64, three, one);
+            };
+            arrive();
+            if constexpr (weigh_turns<D>()) {
+                turn(seg, seg, zero, no, yes, s1, s0);
+                each(1, [&](int r, auto buf, auto odd) ATTN_INLINE {
+                    arrive();
+                    if constexpr (odd)
+                        turn(r, seg, buf, yes, yes, s0, s1);
+                    else
+                        turn(r, seg, buf, yes, yes, s1, s0);
+                });
+                if (tiles & 1)
+                    turn(seg + 32 * tiles, seg, zero, yes, no, s0, s1);
+                else
+                    turn(seg + 32 * tiles, seg, zero, yes, no, s1, s0);
+            } else {
+                turn(seg, seg, zero, no, yes, s0, s0);
+                turn(seg + 32, seg, zero, yes, no, s0, s0);
+                each(1, [&](int r, auto buf, auto) ATTN_INLINE {
+                    arrive();
+                    turn(r, seg, buf, no, yes, s0, s0);
+                    turn(r + 32, seg, buf, yes, no, s0, s0);
+                });
             }
         }
-#pragma unroll
-        for (int p = 0; p < NC; p++) {
-            sum[p] += __shfl_xor(sum[p], 32, 64);
-            const int t = tw + 32 * p + col;
-            if (e != 0 || t >= s.kv)
-                continue;
+        wait_vm<0>();
+        sum += __shfl_xor(sum, 32, 64);
+        if (e == 0 && token < s.kv) {
             if (splits > 1) {
                 // [sequence's units in a row: block, head][split][token of the block]
                 const int64_t unit = f.before.units + (int64_t)block * a.kv_heads + h;
-                w.partial[(unit * splits + split) * BT + (t - t0)] = sum[p];
-                continue;
+                w.partial[(unit * splits + split) * BT + (token - t0)] = sum;
+            } else {
+                weigh_put(w, table, h, token, s.kv - s.nq, sum);
             }
-            weigh_put(w, table, h, t, s.kv - s.nq, sum[p]);
         }
     }
 }
 
 // Adds the parts of split blocks, in order; a workgroup a block and KV head at a time.
 template <int D>
-__global__ void __launch_bounds__(128 * weigh_cols<D>())
+__global__ void __launch_bounds__(weigh_block<D>())
 weigh_join_kernel(WeighArgs w)
 {
     constexpr int BT = weigh_block<D>();

@@ -121,7 +121,7 @@ def test_chunks_on_a_context(D, causal):
 
 @pytest.mark.parametrize("D", [64, 256])
 def test_many_rows(D):
-    """More rows of a sequence than their shifts' space in shared memory holds (2048 at a time)."""
+    """More rows of a sequence than their shifts' space in shared memory holds (1024 at a time)."""
     check(make([700, 40], [760, 300], 1, 7, D, 16, seed=2), f"many rows D={D}")
 
 
