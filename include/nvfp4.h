@@ -122,8 +122,9 @@ enum {
     NVFP4_OP_MOE = 3,      /* nvfp4_moe_grouped_gemm                */
     NVFP4_OP_MOE_ROUTE = 4, /* nvfp4_moe_route / the staged GEMMs   */
     NVFP4_OP_MX_MOE = 5,    /* mx_moe_w4a8                          */
-    NVFP4_OP_KV_ATTENTION = 6, /* nvfp4_kv_attention, .._tree       */
-    NVFP4_OP_KV_WEIGHTS = 7   /* nvfp4_kv_weights                   */
+    NVFP4_OP_KV_ATTENTION = 6, /* nvfp4_kv_attention                */
+    NVFP4_OP_KV_ATTENTION_TREE = 7, /* nvfp4_kv_attention_tree      */
+    NVFP4_OP_KV_WEIGHTS = 8   /* nvfp4_kv_weights                   */
 };
 
 /* Bytes of `ws` an operation needs.  Unused arguments may be 0:
@@ -131,8 +132,8 @@ enum {
  *   GEMM: T = M (rows of A), H = K, I = N (rows of W); non-zero only for
  *         few-row shapes whose K is split over several workgroups.
  *   MOE, MOE_ROUTE: T tokens, k slots, E experts, H hidden, I intermediate.
- *   KV_ATTENTION, KV_WEIGHTS: T = n (query rows), k = q_heads, E = kv_heads,
- *         H = head_dim, I = seqs. */
+ *   KV_ATTENTION, KV_ATTENTION_TREE, KV_WEIGHTS: T = n (query rows), k =
+ *         q_heads, E = kv_heads, H = head_dim, I = seqs. */
 size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 
 /*
@@ -599,6 +600,8 @@ nvfp4_status nvfp4_kv_attention(const void* q_bf16, int64_t ld_q, int64_t n, int
  * A sequence with fewer cached tokens than query rows has no tokens before the
  * drafts, and of these only the last kv_lens[b].  Table entries of pages that lie
  * wholly more than `window` tokens before the drafts may hold anything.
+ *   ws: nvfp4_workspace_size(NVFP4_OP_KV_ATTENTION_TREE, n, q_heads, kv_heads, D,
+ *   seqs) bytes, 256-byte aligned.
  */
 nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads,
                                      const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,

@@ -633,7 +633,8 @@ def _kv_attention(q, k_cache, v_cache, heads, block_table, kv_lens, page_size, c
     if ws is not None:
         _operand(ws, "ws", torch.uint8, 1, device)
     else:
-        need = lib.nvfp4_workspace_size(_lib.OP_KV_ATTENTION, n, q_heads, heads, D, seqs)
+        need = lib.nvfp4_workspace_size(_lib.OP_KV_ATTENTION if mask is None else _lib.OP_KV_ATTENTION_TREE, n, q_heads,
+                                        heads, D, seqs)
         ws = _workspace(need, device) if need else None
     kc, vc = k_cache.c(), v_cache.c()
     scale = D ** -0.5 if scale is None else scale

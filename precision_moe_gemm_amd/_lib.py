@@ -19,7 +19,8 @@ _lib = None
 
 OK, INVALID_ARG, SHAPE, RANGE, WORKSPACE, DEVICE, UNSUPPORTED, DATA = range(8)
 F32, BF16 = 0, 1
-OP_QUANTIZE, OP_REMAP, OP_GEMM, OP_MOE, OP_MOE_ROUTE, OP_MX_MOE, OP_KV_ATTENTION, OP_KV_WEIGHTS = range(8)
+OP_QUANTIZE, OP_REMAP, OP_GEMM, OP_MOE, OP_MOE_ROUTE, OP_MX_MOE, OP_KV_ATTENTION, \
+    OP_KV_ATTENTION_TREE, OP_KV_WEIGHTS = range(9)
 
 
 class NVFP4TensorC(ctypes.Structure):

@@ -1076,6 +1076,22 @@ attn_combine_kernel(AttnArgs a, int pieces)
 // ---------------------------------------------------------------------------
 constexpr int kTileTok = 64;
 
+// TREE: the work of each of a sequence's tiles, in blocks of tokens, and the shares that the work of all tiles is
+// cut into.  Starting and ending a tile counts as kTileStart blocks, which come first, so that shares of many
+// short tiles take no longer than those of a long one.
+constexpr int kTileStart = 4;
+NVFP4_DEV int attn_tile_units(const AttnArgs& a, const AttnSeq& s)
+{
+    const int base = attn_tree_base(s), b0 = a.window > 0 && base > a.window ? (base - a.window) / kTileTok : 0;
+    return (s.kv + kTileTok - 1) / kTileTok - b0 + kTileStart;
+}
+
+NVFP4_DEV int attn_tile_shares(const AttnArgs& a, int total)
+{
+    const int most = (total + kTileStart) / (kTileStart + 1);
+    return most < a.workers ? most : a.workers;
+}
+
 // Place (in 16-byte chunks) of chunk c of row r in the f16 tiles, rows of C
 // chunks: the XOR spreads both the operand reads (32 consecutive rows, one
 // chunk) and the writes over the banks.
@@ -1193,34 +1209,76 @@ attn_tile_kernel(AttnArgs a)
     __shared__ __attribute__((aligned(16))) u32x4 lk0[kTileTok * KC], lk1[kTileTok * KC];
     __shared__ __attribute__((aligned(16))) u32x4 lv0[D * 8], lv1[D * 8];
     __shared__ __attribute__((aligned(16))) int lok[2][4];  // which 16 tokens lie in a page of the cache
-    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, e = lane >> 5;
-    const int wave = uniform(tid >> 6);
-    // ---- the tile: heavy ones first (causal tiles grow towards the end)
+    // ---- the tile: heavy ones first (causal tiles grow towards the end).  TREE: a share of the blocks of all
+    // tiles, as in the row kernel: the tiles are few and their contexts unlike
     const int h = blockIdx.x % a.kv_heads;
-    const int split = blockIdx.y;
+    const int split = TREE ? 0 : blockIdx.y;
     AttnSeq own{0, 0, 0, false};
     auto count = [&](int b) ATTN_INLINE {
         own = attn_seq(a, b);
-        return AttnCount{(own.nq * a.group + ROWS - 1) / ROWS, 1, own.down};
+        return AttnCount{(own.nq * a.group + ROWS - 1) / ROWS, TREE ? attn_tile_units(a, own) : 1, own.down};
     };
     const AttnScan scan = attn_scan(a.seqs, count);
     const int slot = blockIdx.x / a.kv_heads;
-    if (gridDim.y > 1 && blockIdx.x == 0 && split == 0 && tid == 0)
-        a.tiles[0].parts = scan.units;
-    if (slot >= scan.units)
+    if ((TREE || gridDim.y > 1) && blockIdx.x == 0 && split == 0 && threadIdx.x == 0)
+        a.tiles[0].parts = TREE ? scan.tiles : scan.units;
+    const int total = scan.units, shares = TREE ? attn_tile_shares(a, total) : 1;
+    if (slot >= (TREE ? shares : total))
         return;
-    const int tile_no = scan.units - 1 - slot;
-    const AttnFound f = attn_find(scan, a.seqs, tile_no, count);
-    const AttnSeq s = attn_seq_uniform(a, own, f.seq);
-    const int row0 = f.at * ROWS;
+    int unit = TREE ? uniform((int)((int64_t)slot * total / shares)) : total - 1 - slot;
+    const int unit_end = TREE ? uniform((int)((int64_t)(slot + 1) * total / shares)) : unit + 1;
+    AttnFound f = attn_find(scan, a.seqs, unit, count);
+    do {
+    // (TREE: what depends on the lane is computed again for every tile; kept over all of them it took 200
+    // registers more than there are)
+    int tid = threadIdx.x;
+    if constexpr (TREE)
+        asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, col = lane & 31, e = lane >> 5;
+    const int wave = uniform(tid >> 6);
+    AttnSeq s;
+    if constexpr (TREE) {
+        s = attn_seq(a, f.seq);
+        s = AttnSeq{uniform(s.q0), uniform(s.nq), uniform(s.kv), false};
+    } else {
+        s = attn_seq_uniform(a, own, f.seq);
+    }
+    const int units = TREE ? uniform(attn_tile_units(a, s)) : 1;
+    const int tile = TREE ? uniform(f.at / units) : f.at;
+    if (TREE && tile * ROWS >= s.nq * a.group) {
+        f.before.tiles += tile;
+        f.seq++;
+        f.at = 0;
+        continue;
+    }
+    const int row0 = tile * ROWS;
     int lo0, hi0, lo1, hi1;  // tokens of the tile's first and last row
     const int last = (row0 + ROWS - 1) / a.group;
     attn_span<TREE>(a, s, row0 / a.group, last < s.nq ? last : s.nq - 1, &lo0, &hi0, &lo1, &hi1);
-    if constexpr (TREE)
-        attn_tree_check(a, s);
+    const int tile_no = TREE ? f.before.tiles + tile : unit;
     // ---- this split's blocks [b0, b1) of the tile's
     int b0 = lo0 / kTileTok, b1 = hi1 > lo0 ? (hi1 + kTileTok - 1) / kTileTok : b0;
-    if (gridDim.y > 1) {
+    const int first = TREE ? f.at - tile * units : 0;  // the share's part of the tile's work
+    const int part = TREE && units - first > unit_end - unit ? unit_end - unit : units - first;
+    if constexpr (TREE) {
+        attn_tree_check(a, s);
+        const int from = first - kTileStart, to = from + part;
+        b1 = b0 + (to > 0 ? to : 0);
+        b0 += from > 0 ? from : 0;
+        // (`parts` is the last share here: no division where registers are scarce)
+        if (h == 0 && tid == 0) {
+            int* const t = &a.tiles[1 + tile_no].first;
+            if (first == 0) {
+                t[0] = slot;
+                t[2] = s.q0;
+                t[3] = s.nq;
+                t[4] = row0;
+            }
+            if (first + part == units)
+                t[1] = slot;
+        }
+        lds_barrier();  // nobody reads the last tile's blocks any more
+    } else if (gridDim.y > 1) {
         const int n = b1 - b0, per = (n + (int)gridDim.y - 1) / (int)gridDim.y;
         const int base = b0;
         b0 = base + split * per < b1 ? base + split * per : b1;
@@ -1519,8 +1577,40 @@ attn_tile_kernel(AttnArgs a)
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
+    // TREE: waves without a row (a tree's tiles are often partly filled) only decode
+    const bool idle = TREE && row0 + 32 * wave >= s.nq * a.group;
     if (b0 < b1) {
-        if constexpr (!kTurns) {
+        if (TREE && idle && (!kTurns || wave >= NW / 2)) {
+            auto turn = [&](int blk, auto buf) ATTN_INLINE {
+                constexpr std::integral_constant<int, 1 - decltype(buf)::value> other{};
+                lds_barrier();
+                interleave();
+                for_range<0, Raw::kUnits>([&](auto u) ATTN_INLINE {
+                    if constexpr (!kTurns)
+                        decode_k(other, u);
+                    decode_v(other, u);
+                });
+                if constexpr (!kTurns) {
+                    load_k(blk + 2);
+                    pages_k(blk + 3);
+                }
+                load_v(blk + 2);
+                pages_v(blk + 3);
+                if constexpr (kTurns)
+                    lds_barrier();
+            };
+            if constexpr (kTurns) {
+                prepare(no, yes);
+                lds_barrier();
+            } else {
+                prepare(yes, yes);
+            }
+            for (int blk = b0; blk < b1; blk += 2) {
+                turn(blk, zero);
+                if (blk + 1 < b1)
+                    turn(blk + 1, one);
+            }
+        } else if constexpr (!kTurns) {
             prepare(yes, yes);
             auto turn = [&](int blk, auto buf) ATTN_INLINE {
                 lds_barrier();  // the block is written, and nobody reads the other buffer any more
@@ -1568,12 +1658,15 @@ attn_tile_kernel(AttnArgs a)
     l += __shfl_xor(l, 32, 64);
     const int head = h * a.group + hh;
     const int64_t token = s.q0 + qi;
-    if (gridDim.y > 1) {
-        // (m, l, o) of this split: [tile][kv head][split][row][D + 4]
-        if (split == 0 && h == 0 && tid == 0)
+    if (TREE ? part < units : gridDim.y > 1) {
+        // (m, l, o) of this split: [tile][kv head][split][row][D + 4]; TREE: [share][kv head][slot], slot 1 for the
+        // tile's first share
+        if (!TREE && split == 0 && h == 0 && tid == 0)
             a.tiles[1 + tile_no] = AttnTile{0, (int)gridDim.y, s.q0, s.nq, row0};
         if (in) {
-            float* dst = a.partial + ((((int64_t)tile_no * a.kv_heads + h) * gridDim.y + split) * ROWS + 32 * wave + col) * (D + 4);
+            const int64_t at = TREE ? ((int64_t)slot * a.kv_heads + h) * 2 + (first == 0)
+                                    : ((int64_t)tile_no * a.kv_heads + h) * gridDim.y + split;
+            float* dst = a.partial + (at * ROWS + 32 * wave + col) * (D + 4);
             if (e == 0) {
                 dst[D] = m;
                 dst[D + 1] = l;
@@ -1585,26 +1678,27 @@ attn_tile_kernel(AttnArgs a)
                     *(float4_t*)(dst + 32 * d + 8 * i + 4 * e) =
                         (float4_t){o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
         }
-        return;
+    } else if (in) {
+        const float g = l != 0.0f ? *a.v_global / l : 0.0f;
+        uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + 4 * e;
+#pragma unroll
+        for (int d = 0; d < D / 32; d++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                *(u32x2*)(dst + 32 * d + 8 * i) = (u32x2){pack_bf16x2(o[d][4 * i] * g, o[d][4 * i + 1] * g),
+                                                          pack_bf16x2(o[d][4 * i + 2] * g, o[d][4 * i + 3] * g)};
+        if (a.lse && e == 0)
+            a.lse[token * (a.kv_heads * a.group) + head] =
+                l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
     }
-    if (!in)
-        return;
-    const float g = l != 0.0f ? *a.v_global / l : 0.0f;
-    uint16_t* dst = a.out + token * a.ld_out + (int64_t)head * D + 4 * e;
-#pragma unroll
-    for (int d = 0; d < D / 32; d++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            *(u32x2*)(dst + 32 * d + 8 * i) = (u32x2){pack_bf16x2(o[d][4 * i] * g, o[d][4 * i + 1] * g),
-                                                      pack_bf16x2(o[d][4 * i + 2] * g, o[d][4 * i + 3] * g)};
-    if (a.lse && e == 0)
-        a.lse[token * (a.kv_heads * a.group) + head] =
-            l != 0.0f ? (m - kAttnLift + __builtin_amdgcn_logf(l)) * 0.69314718056f : -__builtin_inff();
+    unit += part;
+    f.at += part;
+    } while (TREE && unit < unit_end);
 }
 
-// Joins the splits of a tile of ROWS rows (blockIdx.x) and KV head
-// (blockIdx.y): a wave a row at a time.
-template <int D, int ROWS>
+// Joins the splits (TREE: the shares) of a tile of ROWS rows (blockIdx.x) and KV
+// head (blockIdx.y): a wave a row at a time.
+template <int D, int ROWS, bool TREE>
 __global__ void __launch_bounds__(256)
 attn_tile_combine_kernel(AttnArgs a)
 {
@@ -1612,22 +1706,26 @@ attn_tile_combine_kernel(AttnArgs a)
     const int tiles = a.tiles[0].parts;
     const AttnTile tile = a.tiles[1 + blockIdx.x];
     const float vg = *a.v_global;
-    if ((int)blockIdx.x >= tiles)
+    const int first = uniform(tile.first), parts = uniform(tile.parts) - (TREE ? first - 1 : 0);
+    if ((int)blockIdx.x >= tiles || (TREE && parts == 1))
         return;
-    const int h = blockIdx.y, parts = uniform(tile.parts);
+    const int h = blockIdx.y;
     constexpr int V = D / 64;  // elements per lane
     for (int row = blockIdx.z * 4 + wave; row < ROWS; row += gridDim.z * 4) {
         const int r = tile.row0 + row, i = r / a.group, head = h * a.group + r - i * a.group;
         if (i >= tile.nq)
             break;
-        const float* src = a.partial + (((int64_t)blockIdx.x * a.kv_heads + h) * parts * ROWS + row) * (D + 4);
+        // (TREE: slot 1 of the tile's first share, slot 0 of the others)
+        const int64_t at = TREE ? ((int64_t)first * a.kv_heads + h) * 2 : ((int64_t)blockIdx.x * a.kv_heads + h) * parts;
+        const float* src = a.partial + (at * ROWS + row) * (D + 4);
+        const int64_t step = (int64_t)(TREE ? 2 * a.kv_heads : 1) * ROWS * (D + 4);
         float m = kAttnLow, l = 0.0f, o[V];
 #pragma unroll
         for (int j = 0; j < V; j++)
             o[j] = 0.0f;
 #pragma unroll 4
         for (int p = 0; p < parts; p++) {
-            const float* x = src + (int64_t)p * ROWS * (D + 4);
+            const float* x = src + p * step + (TREE && p == 0 ? ROWS * (D + 4) : 0);
             const float om = x[D], ol = x[D + 1], now = __builtin_fmaxf(m, om);
             const float f = __builtin_amdgcn_exp2f(m - now), g = __builtin_amdgcn_exp2f(om - now);
             l = l * f + ol * g;

@@ -275,6 +275,13 @@ int64_t attention_tile_splits(int64_t tiles, int kv_heads)
     return std::max<int64_t>(1, 256 / std::max<int64_t>(1, tiles * kv_heads));
 }
 
+// Shares of the tile kernel for trees, per KV head: as many as workgroups are resident.
+template <int D, int NW>
+int attention_tile_workers(int kv_heads)
+{
+    return std::max(1, (NW == 8 || D == 256 ? 256 : 512) / kv_heads);
+}
+
 size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64_t seqs)
 {
     const int hl = attention_head_lanes(kv_heads);
@@ -286,6 +293,19 @@ size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64
         const int64_t splits = attention_tile_splits(tiles, kv_heads);
         if (splits > 1)
             part = std::max(part, (size_t)(tiles * kv_heads * splits * rows * (D + 4)) * sizeof(float));
+    }
+    return attention_tiles_bytes(n, q_heads / kv_heads, seqs) + align256(part);
+}
+
+size_t attention_tree_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64_t seqs)
+{
+    // row kernel: as without trees; tile kernel: two slots per share, its rows of D + 4 values
+    const int hl = attention_head_lanes(kv_heads);
+    const size_t rows = (size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float);
+    size_t part = rows;
+    for (int w = 128; w <= 256; w *= 2) {
+        const int64_t workers = std::max(1, (w == 256 || D == 256 ? 256 : 512) / kv_heads);
+        part = std::max(part, (size_t)(workers * kv_heads * 2 * w * (D + 4)) * sizeof(float));
     }
     return attention_tiles_bytes(n, q_heads / kv_heads, seqs) + align256(part);
 }
@@ -343,13 +363,25 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
     const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, ROWS);  // (the workspace's count: it sets the splits)
     if (tiles * a.kv_heads * 64 * NW > 0xFFFFFFFF)  // threads of one dimension of a launch
         return NVFP4_ERR_UNSUPPORTED;
+    if (TREE) {
+        AttnArgs b = a;
+        b.workers = attention_tile_workers<D, NW>(a.kv_heads);
+        if (tiles * (ceil_div((int64_t)a.pages * a.page, kTileTok) + kTileStart) > 0x7FFFFFFF)
+            return NVFP4_ERR_UNSUPPORTED;
+        attn_tile_kernel<D, NW, true><<<(unsigned)(b.workers * a.kv_heads), 64 * NW, 0, st>>>(b);
+        nvfp4_status s = launch_status();
+        if (s != NVFP4_OK)
+            return s;
+        attn_tile_combine_kernel<D, ROWS, true><<<dim3((unsigned)tiles, a.kv_heads, ROWS / 16), 256, 0, st>>>(b);
+        return launch_status();
+    }
     const int64_t splits = std::min(attention_tile_splits(tiles, a.kv_heads),
                                     std::max<int64_t>(1, (int64_t)a.pages * a.page / (4 * kTileTok)));
-    attn_tile_kernel<D, NW, TREE><<<dim3((unsigned)(tiles * a.kv_heads), (unsigned)splits), 64 * NW, 0, st>>>(a);
+    attn_tile_kernel<D, NW, false><<<dim3((unsigned)(tiles * a.kv_heads), (unsigned)splits), 64 * NW, 0, st>>>(a);
     nvfp4_status s = launch_status();
     if (s != NVFP4_OK || splits == 1)
         return s;
-    attn_tile_combine_kernel<D, ROWS><<<dim3((unsigned)tiles, a.kv_heads, 8), 256, 0, st>>>(a);
+    attn_tile_combine_kernel<D, ROWS, false><<<dim3((unsigned)tiles, a.kv_heads, 8), 256, 0, st>>>(a);
     return launch_status();
 }
 
@@ -1267,6 +1299,10 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
             return 0;
         return attention_ws_bytes(T, k, E, H, I);
+    case NVFP4_OP_KV_ATTENTION_TREE:
+        if (T <= 0 || k < 1 || E < 1 || H <= 0 || I <= 0)
+            return 0;
+        return attention_tree_ws_bytes(T, k, E, H, I);
     case NVFP4_OP_KV_WEIGHTS:
         if (T <= 0 || H <= 0 || I <= 0)
             return 0;
@@ -2422,7 +2458,8 @@ static nvfp4_status kv_attention(const void* q, int64_t ld_q, int64_t n, int32_t
     // (a row's 16 scale bytes are one copy)
     if (D == 256 && (!aligned(k_cache->scales, 16) || !aligned(v_cache->scales, 16)))
         return NVFP4_ERR_INVALID_ARG;
-    const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_ATTENTION, n, q_heads, kv_heads, D, seqs);
+    const size_t need = nvfp4_workspace_size(tree ? NVFP4_OP_KV_ATTENTION_TREE : NVFP4_OP_KV_ATTENTION, n, q_heads, kv_heads,
+                                             D, seqs);
     if (need > 0 && (!ws || !aligned(ws, 256)))
         return NVFP4_ERR_INVALID_ARG;
     if (ws_bytes < need)

@@ -16,7 +16,7 @@ def tree(lib, **kw):
     from precision_moe_gemm_amd import _lib as L
     a = dict(TREE, **kw)
     kc, vc = a["kc"] or cache(), a["vc"] or cache()
-    need = lib.nvfp4_workspace_size(L.OP_KV_ATTENTION, max(a["n"], 0), max(a["q_heads"], 0), a["heads"], kc.cols,
+    need = lib.nvfp4_workspace_size(L.OP_KV_ATTENTION_TREE, max(a["n"], 0), max(a["q_heads"], 0), a["heads"], kc.cols,
                                     max(a["seqs"], 0))
     return lib.nvfp4_kv_attention_tree(a["q"], a["ld_q"], a["n"], a["q_heads"], ctypes.byref(kc), ctypes.byref(vc),
                                        a["heads"], a["table"], a["ld_table"], a["pages"], a["page"], a["lens"], a["cu"],

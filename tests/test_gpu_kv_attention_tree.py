@@ -229,7 +229,7 @@ def test_another_stream_graph_replays_and_a_workspace_each():
         out, lse = call(c)
     torch.cuda.current_stream().wait_stream(side)
     assert_attention(out, lse, reference(c), "another stream")
-    need = nv.nvfp4_workspace_size(nv._lib.OP_KV_ATTENTION, 32, 8, 2, 128, 3)
+    need = nv.nvfp4_workspace_size(nv._lib.OP_KV_ATTENTION_TREE, 32, 8, 2, 128, 3)
     graphs = []
     for max_q in (9, 40):
         ws = torch.empty(need, dtype=torch.uint8, device=DEV)
