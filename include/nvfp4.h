@@ -124,7 +124,8 @@ enum {
     NVFP4_OP_MX_MOE = 5,    /* mx_moe_w4a8                          */
     NVFP4_OP_KV_ATTENTION = 6, /* nvfp4_kv_attention                */
     NVFP4_OP_KV_ATTENTION_TREE = 7, /* nvfp4_kv_attention_tree      */
-    NVFP4_OP_KV_WEIGHTS = 8   /* nvfp4_kv_weights                   */
+    NVFP4_OP_KV_WEIGHTS = 8,  /* nvfp4_kv_weights                   */
+    NVFP4_OP_KV_SELECT = 9    /* nvfp4_kv_select                    */
 };
 
 /* Bytes of `ws` an operation needs.  Unused arguments may be 0:
@@ -133,7 +134,8 @@ enum {
  *         few-row shapes whose K is split over several workgroups.
  *   MOE, MOE_ROUTE: T tokens, k slots, E experts, H hidden, I intermediate.
  *   KV_ATTENTION, KV_ATTENTION_TREE, KV_WEIGHTS: T = n (query rows), k =
- *         q_heads, E = kv_heads, H = head_dim, I = seqs. */
+ *         q_heads, E = kv_heads, H = head_dim, I = seqs.
+ *   KV_SELECT: E = kv_heads, H = pages_per_seq * page_size, I = seqs. */
 size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, int64_t I);
 
 /*
@@ -663,7 +665,10 @@ nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32
  *   moves: int32 [seqs, kv_heads, cap, 2]: (source, destination) places, -1, -1
  *   behind the last; cap >= min(keep, pages_per_seq * page_size - keep), else
  *   NVFP4_ERR_SHAPE;
- *   lens_out: int32 [seqs], min(kv_lens[b], keep); not kv_lens itself.
+ *   lens_out: int32 [seqs], min(kv_lens[b], keep); not kv_lens itself;
+ *   ws: nvfp4_workspace_size(NVFP4_OP_KV_SELECT, 0, 0, kv_heads, pages_per_seq *
+ *   page_size, seqs) bytes, 256-byte aligned (may be NULL if that is 0, as it is
+ *   for rows of the table of up to 32768 tokens).
  * Nothing is moved, and weights are not changed.  keep >= 1, sinks + recent <=
  * keep (else NVFP4_ERR_INVALID_ARG).  A kv_lens[b] outside the table's places is
  * cut and raises the sticky NVFP4_ERR_RANGE, as does an entry that is not a page
@@ -673,7 +678,8 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
                              int32_t kv_heads, int64_t tokens, const int32_t* block_table, int64_t ld_table,
                              int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
                              const int32_t* next_positions, int32_t seqs, int32_t keep, int32_t sinks, int32_t recent,
-                             int32_t* moves, int32_t cap, int32_t* lens_out, void* stream);
+                             int32_t* moves, int32_t cap, int32_t* lens_out, void* ws, size_t ws_bytes,
+                             void* stream);
 
 /*
  * Move cached tokens within their sequences: K and V (codes and scales), and

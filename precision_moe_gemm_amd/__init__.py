@@ -734,7 +734,7 @@ def nvfp4_kv_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: NVFP4Tensor, h
 
 def nvfp4_kv_select(weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int, keep: int,
                     positions: torch.Tensor | None = None, next_positions: torch.Tensor | None = None, sinks: int = 0,
-                    recent: int = 0, cap: int | None = None):
+                    recent: int = 0, cap: int | None = None, ws: torch.Tensor | None = None):
     """(moves, lens): the moves (int32 [seqs, heads, cap, 2], pairs of places, -1
     behind the last) after which each KV head of a sequence of more than `keep`
     tokens has the tokens that it keeps at its first `keep` places, and the lengths
@@ -762,11 +762,17 @@ def nvfp4_kv_select(weights: torch.Tensor, block_table: torch.Tensor, kv_lens: t
         raise ValueError(f"cap: {cap}")
     moves = torch.empty((seqs, heads, cap, 2), dtype=torch.int32, device=device)
     lens = torch.empty((seqs,), dtype=torch.int32, device=device)
+    lib = _lib.load()
+    if ws is not None:
+        _operand(ws, "ws", torch.uint8, 1, device)
+    else:
+        need = lib.nvfp4_workspace_size(_lib.OP_KV_SELECT, 0, 0, heads, pages * page_size, seqs)
+        ws = _workspace(need, device) if need else None
     with _on(device):
-        st = _lib.load().nvfp4_kv_select(
+        st = lib.nvfp4_kv_select(
             _ptr(weights), ld_w, _ptr(positions), ld_p, heads, tokens, _ptr(block_table), ld_table, pages, page_size,
             _ptr(kv_lens), None if positions is None else _ptr(next_positions), seqs, keep, sinks, recent, _ptr(moves),
-            cap, _ptr(lens), _stream(device))
+            cap, _ptr(lens), _ptr(ws), 0 if ws is None else ws.numel(), _stream(device))
     _check(st, "nvfp4_kv_select")
     return moves, lens
 

@@ -20,7 +20,7 @@ _lib = None
 OK, INVALID_ARG, SHAPE, RANGE, WORKSPACE, DEVICE, UNSUPPORTED, DATA = range(8)
 F32, BF16 = 0, 1
 OP_QUANTIZE, OP_REMAP, OP_GEMM, OP_MOE, OP_MOE_ROUTE, OP_MX_MOE, OP_KV_ATTENTION, \
-    OP_KV_ATTENTION_TREE, OP_KV_WEIGHTS = range(9)
+    OP_KV_ATTENTION_TREE, OP_KV_WEIGHTS, OP_KV_SELECT = range(10)
 
 
 class NVFP4TensorC(ctypes.Structure):
@@ -80,7 +80,8 @@ SIGNATURES = {
                                      ctypes.c_float, I32, P, I64, P, P, SZ, P]),
     "nvfp4_kv_weights": (ST, [P, I64, I64, I32, P, TP, I32, P, I64, I32, I32, P, P, I32, I32, ctypes.c_float, I32, I32, P,
                               I64, P, I64, P, SZ, P]),
-    "nvfp4_kv_select": (ST, [P, I64, P, I64, I32, I64, P, I64, I32, I32, P, P, I32, I32, I32, I32, P, I32, P, P]),
+    "nvfp4_kv_select": (ST, [P, I64, P, I64, I32, I64, P, I64, I32, I32, P, P, I32, I32, I32, I32, P, I32, P, P, SZ,
+                             P]),
     "nvfp4_kv_move": (ST, [TP, TP, I32, P, I64, I32, I32, I32, P, I32, I32, P, I64, P, I64, P]),
     "mxfp8_add_rmsnorm": (ST, [P, I64, P, I64, P, ctypes.c_double, I64, I64, P, I64, P, I64, P, P, P]),
     "nvfp4_audit_scales": (ST, [TP, P, P]),

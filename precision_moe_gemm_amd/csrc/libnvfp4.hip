@@ -477,13 +477,55 @@ nvfp4_status launch_weights(const WeighArgs& w, int64_t max_q, hipStream_t st)
     return launch_status();
 }
 
-void launch_select(const SelectArgs& s, hipStream_t st)
+// The workspace of longer rows of the table (none for those whose keys fit the shared memory of a workgroup).
+struct SelectLayout {
+    int64_t shares, span;
+    size_t keys, some, counts, coarse, share, found, end;
+};
+
+SelectLayout select_layout(int64_t lists, int64_t places)
 {
-    const unsigned grid = (unsigned)(s.a.seqs * s.a.kv_heads);
-    if ((int64_t)s.a.pages * s.a.page <= 4096)
-        select_kernel<4096><<<grid, kSelectThreads, 0, st>>>(s);
-    else
-        select_kernel<32768><<<grid, kSelectThreads, 0, st>>>(s);
+    SelectLayout y{};
+    if (places <= kSelectHeld)
+        return y;
+    // (4096 workgroups at most, of at least kSelectSpan tokens)
+    y.shares = std::min<int64_t>({ceil_div(places, kSelectSpan), std::max<int64_t>(1, 4096 / lists), kSelectShares});
+    y.span = ceil_div(ceil_div(places, y.shares), 256) * 256;
+    y.some = align256((size_t)(lists * places) * sizeof(uint32_t));
+    y.counts = 2 * y.some;
+    y.coarse = y.counts + (size_t)(lists * y.shares) * 2048 * sizeof(uint32_t);
+    y.share = y.coarse + (size_t)(lists * y.shares) * 64 * sizeof(uint32_t);
+    y.found = align256(y.share + (size_t)(lists * y.shares) * sizeof(SelectShare));
+    y.end = align256(y.found + (size_t)lists * sizeof(SelectFound));
+    return y;
+}
+
+nvfp4_status launch_select(SelectArgs s, uint8_t* ws, hipStream_t st)
+{
+    const int64_t lists = (int64_t)s.a.seqs * s.a.kv_heads, places = (int64_t)s.a.pages * s.a.page;
+    if (places <= 4096) {
+        select_kernel<256, 4096><<<(unsigned)lists, 256, 0, st>>>(s);
+        return launch_status();
+    }
+    if (places <= kSelectHeld) {
+        select_kernel<1024, kSelectHeld><<<(unsigned)lists, 1024, 0, st>>>(s);
+        return launch_status();
+    }
+    const SelectLayout y = select_layout(lists, places);
+    s.shares = (int)y.shares;
+    s.span = (int)y.span;
+    s.keys = (uint32_t*)ws;
+    s.some = (uint32_t*)(ws + y.some);
+    s.counts = (uint32_t*)(ws + y.counts);
+    s.coarse = (uint32_t*)(ws + y.coarse);
+    s.share = (SelectShare*)(ws + y.share);
+    s.found = (SelectFound*)(ws + y.found);
+    const dim3 grid((unsigned)lists, (unsigned)y.shares);
+    select_keys_kernel<<<grid, kSelectThreads, 0, st>>>(s);
+    select_some_kernel<<<grid, kSelectThreads, 0, st>>>(s);
+    select_last_kernel<<<(unsigned)lists, 1024, 0, st>>>(s);
+    select_moves_kernel<<<grid, kSelectThreads, 0, st>>>(s);
+    return launch_status();
 }
 
 void launch_move(const MoveArgs& m, hipStream_t st)
@@ -1307,6 +1349,11 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
         if (T <= 0 || H <= 0 || I <= 0)
             return 0;
         return weights_ws_bytes(H);
+    case NVFP4_OP_KV_SELECT:
+        // E KV heads, H = tokens of a row of the table, I = sequences
+        if (E < 1 || H <= 0 || I <= 0)
+            return 0;
+        return select_layout((int64_t)E * I, H).end;
     }
     return 0;
 }
@@ -2620,7 +2667,7 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
                              int32_t kv_heads, int64_t tokens, const int32_t* block_table, int64_t ld_table,
                              int32_t pages_per_seq, int32_t page_size, const int32_t* kv_lens,
                              const int32_t* next_positions, int32_t seqs, int32_t keep, int32_t sinks, int32_t recent,
-                             int32_t* moves, int32_t cap, int32_t* lens_out, void* stream)
+                             int32_t* moves, int32_t cap, int32_t* lens_out, void* ws, size_t ws_bytes, void* stream)
 {
     nvfp4_status st = check_pages(tokens, kv_heads, block_table, ld_table, pages_per_seq, page_size, seqs);
     if (st != NVFP4_OK)
@@ -2641,6 +2688,11 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
     // (one KV head's workgroup writes a length that the others read)
     if (rows_share(lens_out, seqs, seqs, kv_lens, seqs, seqs, 1, 4))
         return NVFP4_ERR_INVALID_ARG;
+    const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_SELECT, 0, 0, kv_heads, most, seqs);
+    if (need > 0 && (!ws || !aligned(ws, 256)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (ws_bytes < need)
+        return NVFP4_ERR_WORKSPACE;
     SelectArgs a{};
     set_pages(a.a, block_table, ld_table, pages_per_seq, page_size, kv_lens, seqs, tokens / page_size);
     a.a.kv_heads = kv_heads;
@@ -2655,8 +2707,7 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
     a.moves = moves;
     a.cap = cap;
     a.lens = lens_out;
-    launch_select(a, S(stream));
-    return launch_status();
+    return launch_select(a, (uint8_t*)ws, S(stream));
 }
 
 nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,

@@ -130,14 +130,14 @@ def test_weights_in_place_or_elsewhere(lib):
 
 
 SELECT = dict(w=P(1 << 14), ld_w=64, pos=P(1 << 15), ld_p=64, heads=2, tokens=64, table=P(64), ld_table=3, pages=3, page=16,
-              lens=P(64), next=P(64), seqs=3, keep=20, sinks=2, recent=8, moves=P(4096), cap=20, out=P(8192))
+              lens=P(64), next=P(64), seqs=3, keep=20, sinks=2, recent=8, moves=P(4096), cap=20, out=P(8192), ws=None, ws_bytes=0)
 
 
 def select(lib, **kw):
     a = dict(SELECT, **kw)
     return lib.nvfp4_kv_select(a["w"], a["ld_w"], a["pos"], a["ld_p"], a["heads"], a["tokens"], a["table"], a["ld_table"],
                                a["pages"], a["page"], a["lens"], a["next"], a["seqs"], a["keep"], a["sinks"], a["recent"],
-                               a["moves"], a["cap"], a["out"], None)
+                               a["moves"], a["cap"], a["out"], a["ws"], a["ws_bytes"], None)
 
 
 def test_select_refusals(lib):
@@ -168,6 +168,19 @@ def test_select_refusals(lib):
     assert select(lib, pos=P(66)) == L.INVALID_ARG
     assert select(lib, out=SELECT["lens"]) == L.INVALID_ARG     # other heads still read the lengths
     assert select(lib, out=P(64 + 8)) == L.INVALID_ARG
+
+
+def test_select_workspace(lib):
+    from precision_moe_gemm_amd import _lib as L
+    assert lib.nvfp4_workspace_size(L.OP_KV_SELECT, 0, 0, 2, 32768, 3) == 0
+    need = lib.nvfp4_workspace_size(L.OP_KV_SELECT, 0, 0, 2, 32784, 3)
+    assert need >= 2 * 32784 * 3 * 4 and need % 256 == 0
+    assert lib.nvfp4_workspace_size(L.OP_KV_SELECT, 0, 0, 0, 32784, 3) == 0
+    assert lib.nvfp4_workspace_size(L.OP_KV_SELECT, 0, 0, 2, 32784, -1) == 0
+    wide = dict(tokens=1 << 20, ld_w=1 << 20, ld_p=1 << 20, pages=2049, ld_table=2049, keep=16, sinks=0)
+    assert select(lib, **wide) == L.INVALID_ARG                 # no workspace
+    assert select(lib, ws=P((1 << 20) + 128), ws_bytes=need, **wide) == L.INVALID_ARG
+    assert select(lib, ws=P(1 << 20), ws_bytes=need - 1, **wide) == L.WORKSPACE
 
 
 MOVE = dict(kc=None, vc=None, heads=2, table=P(64), ld_table=2, pages=2, page=16, seqs=3, moves=P(4096), lists=2, cap=5,
