@@ -628,7 +628,8 @@ nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n
  *   same stride (one that shares an element with w otherwise:
  *   NVFP4_ERR_INVALID_ARG).  Written are the cached tokens of the call's sequences
  *   only; in place, tokens before every row's window are left as they are.
- *   max_q: as there (a wrong one costs speed, not results).
+ *   max_q: as there (a wrong one costs speed, not results).  With n = 0 (q and lse
+ *   may be NULL) the weights are copied.
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs)
  *   bytes, 256-byte aligned.
  * Each of the weights counts as a number of [0, 1], a NaN as 0: rows of q with a

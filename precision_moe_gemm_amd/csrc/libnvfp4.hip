@@ -1346,7 +1346,8 @@ size_t nvfp4_workspace_size(int op, int64_t T, int32_t k, int32_t E, int64_t H, 
             return 0;
         return attention_tree_ws_bytes(T, k, E, H, I);
     case NVFP4_OP_KV_WEIGHTS:
-        if (T <= 0 || H <= 0 || I <= 0)
+        // (T may be 0: weights are then copied, by the same launches)
+        if (T < 0 || H <= 0 || I <= 0)
             return 0;
         return weights_ws_bytes(H);
     case NVFP4_OP_KV_SELECT:
@@ -2618,7 +2619,7 @@ nvfp4_status nvfp4_kv_weights(const void* q, int64_t ld_q, int64_t n, int32_t q_
         return NVFP4_ERR_UNSUPPORTED;
     if (ld_q < q_heads * D || ld_q % 8 != 0 || (weights && ld_weights < tokens) || ld_out < tokens)
         return NVFP4_ERR_SHAPE;
-    if (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
+    if ((n > 0 && (!q || !lse)) || !aligned(q, 16) || !aligned(lse, 4) || !kv_lens || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
         !aligned(weights, 4) || !weights_out || !aligned(weights_out, 4))
         return NVFP4_ERR_INVALID_ARG;
     if (rows_clash(weights_out, ld_out, weights, ld_weights, tokens, kv_heads, 4))
@@ -2656,7 +2657,8 @@ nvfp4_status nvfp4_kv_weights(const void* q, int64_t ld_q, int64_t n, int32_t q_
          : D == 128 ? launch_weights<128>(w, max_q, S(stream))
                     : launch_weights<256>(w, max_q, S(stream));
     if (st == NVFP4_OK && checks_on()) {
-        check_bf16(q, n, q_heads * D, ld_q, S(stream));
+        if (n > 0)
+            check_bf16(q, n, q_heads * D, ld_q, S(stream));
         check_globals(k_cache->global, 1, S(stream));
         st = launch_status();
     }

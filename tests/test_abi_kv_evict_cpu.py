@@ -111,6 +111,14 @@ def test_weights_refusals(lib):
     assert weights(lib, kc=wide, ld_q=1024) == L.INVALID_ARG     # 16-byte copies of scales
 
 
+def test_weights_without_query_rows(lib):
+    """They are copied, by launches that need the workspace as well."""
+    from precision_moe_gemm_amd import _lib as L
+    assert lib.nvfp4_workspace_size(L.OP_KV_WEIGHTS, 0, 4, 2, 128, 3) == lib.nvfp4_workspace_size(L.OP_KV_WEIGHTS, 3, 4, 2, 128, 3)
+    assert weights(lib, n=0, cu=P(64), q=None, lse=None, ws=None) == L.INVALID_ARG
+    assert weights(lib, n=0, cu=P(64), q=None, lse=None, ws_bytes=0) == L.WORKSPACE
+
+
 def test_weights_in_place_or_elsewhere(lib):
     """Two rows of 32 numbers: in place with the same stride alone, side by side in one buffer."""
     from precision_moe_gemm_amd import _lib as L

@@ -146,6 +146,47 @@ def test_rows_without_keys(max_q):
     check(c, "rows without keys, not causal", max_q=max_q, causal=False)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tiles_of_many_sequences(D):
+    """More sequences than a wave has lanes, blocks that are and are not split."""
+    r = np.random.default_rng(D)
+    q = [int(v) for v in r.integers(0, 30, 90)]
+    c = make(q, [a + int(v) for a, v in zip(q, r.integers(0, 300, 90))], 1, 3, D, 16, seed=D)
+    check(c, f"90 sequences in tiles D={D}", max_q=200)
+    check(make([1] * 300, [int(v) for v in r.integers(1, 600, 300)], 4, 2, D, 16, seed=D), f"300 sequences D={D}", max_q=200)
+
+
+@pytest.mark.parametrize("max_q", [1, 16, 200])
+def test_many_heads(max_q):
+    check(make([2, 7], [40, 70], 268, 1, 64, 16, seed=5), f"268 KV heads max_q={max_q}", max_q=max_q)
+    check(make([2, 7], [40, 70], 129, 2, 64, 16, seed=5), f"129 KV heads max_q={max_q}", max_q=max_q)
+
+
+@pytest.mark.parametrize("max_q", [1, 32, 200])
+def test_the_widest_window(max_q):
+    c = make([3, 40], [90, 300], 2, 2, 128, 16, seed=37)
+    check(c, f"window=2^31-1 max_q={max_q}", max_q=max_q, window=2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("max_q", [0, 200])
+def test_no_query_rows_at_all(max_q):
+    """The weights are copied, with no query row in the call."""
+    c = make([0, 0], [90, 33], 2, 2, 64, 16, seed=35)
+    c["lse"] = torch.empty((0, 4), device=DEV)
+    step(f"no query rows max_q={max_q}")
+    out = call(c, max_q=max_q)
+    mine = c["before"].clone()
+    call(c, out=mine, weights=mine, max_q=max_q)
+    torch.cuda.synchronize()
+    assert nv.nvfp4_get_error() == 0
+    assert torch.equal(mine, c["before"])
+    own = torch.zeros_like(out, dtype=torch.bool)
+    for b, kv in enumerate((90, 33)):
+        t = torch.arange(kv, device=DEV)
+        own[:, c["table"][b].long()[t // 16] * 16 + t % 16] = True
+    assert torch.equal(out, torch.where(own, c["before"], 7.0))
+
+
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [40, 1, 9]])
 def test_the_sum_over_all_tokens_is_the_number_of_rows(q_lens):
     """No weights before: what a KV head's tokens receive adds up to its rows."""
