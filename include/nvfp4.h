@@ -666,7 +666,7 @@ nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32
  *   moves: int32 [seqs, kv_heads, cap, 2]: (source, destination) places, -1, -1
  *   behind the last; cap >= min(keep, pages_per_seq * page_size - keep), else
  *   NVFP4_ERR_SHAPE;
- *   lens_out: int32 [seqs], min(kv_lens[b], keep); not kv_lens itself;
+ *   lens_out: int32 [seqs], min(kv_lens[b], keep); neither kv_lens nor next_positions;
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_SELECT, 0, 0, kv_heads, pages_per_seq *
  *   page_size, seqs) bytes, 256-byte aligned (may be NULL if that is 0, as it is
  *   for rows of the table of up to 32768 tokens).

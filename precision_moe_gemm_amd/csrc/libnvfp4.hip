@@ -2681,6 +2681,8 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
         return NVFP4_ERR_SHAPE;
     if (seqs == 0)
         return NVFP4_OK;
+    if (cap > 0x3FFFFFFF)  // (the kernels count pairs in 31 bits)
+        return NVFP4_ERR_UNSUPPORTED;
     if (ld_weights < tokens || (positions && ld_positions < tokens))
         return NVFP4_ERR_SHAPE;
     if (!weights || !aligned(weights, 4) || !aligned(positions, 4) || (positions && !next_positions) ||
@@ -2688,7 +2690,8 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
         !lens_out || !aligned(lens_out, 4))
         return NVFP4_ERR_INVALID_ARG;
     // (one KV head's workgroup writes a length that the others read)
-    if (rows_share(lens_out, seqs, seqs, kv_lens, seqs, seqs, 1, 4))
+    if (rows_share(lens_out, seqs, seqs, kv_lens, seqs, seqs, 1, 4) ||
+        (positions && rows_share(lens_out, seqs, seqs, next_positions, seqs, seqs, 1, 4)))
         return NVFP4_ERR_INVALID_ARG;
     const size_t need = nvfp4_workspace_size(NVFP4_OP_KV_SELECT, 0, 0, kv_heads, most, seqs);
     if (need > 0 && (!ws || !aligned(ws, 256)))
@@ -2735,7 +2738,7 @@ nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_ca
         return st;
     if (seqs == 0 || cap == 0 || pages_per_seq == 0)
         return NVFP4_OK;
-    if (D == 0 || D % 32 != 0 || D > 4096)
+    if (D == 0 || D % 32 != 0 || D > 4096 || cap > 0x3FFFFFFF)
         return NVFP4_ERR_UNSUPPORTED;
     if ((weights && ld_weights < tokens) || (positions && ld_positions < tokens))
         return NVFP4_ERR_SHAPE;

@@ -175,6 +175,8 @@ def test_select_refusals(lib):
         assert select(lib, **{name: P(SELECT[name].value + 2)}) == L.INVALID_ARG, name
     assert select(lib, pos=P(66)) == L.INVALID_ARG
     assert select(lib, out=SELECT["lens"]) == L.INVALID_ARG     # other heads still read the lengths
+    assert select(lib, out=P(256), next=P(256)) == L.INVALID_ARG
+    assert select(lib, cap=1 << 30) == L.UNSUPPORTED
     assert select(lib, out=P(64 + 8)) == L.INVALID_ARG
 
 
@@ -224,6 +226,7 @@ def test_move_refusals(lib):
     assert move(lib, kc=cache(batch=3)) == L.SHAPE
     assert move(lib, kc=cache(cols=144), vc=cache(cols=144)) == L.UNSUPPORTED
     assert move(lib, kc=cache(cols=8192), vc=cache(cols=8192)) == L.UNSUPPORTED
+    assert move(lib, cap=1 << 30) == L.UNSUPPORTED
     assert move(lib, kc=cache(packed=4104)) == L.INVALID_ARG
     assert move(lib, vc=cache(flags=L.TILED_SCALES)) == L.UNSUPPORTED
     for name in ("table", "moves"):

@@ -85,6 +85,56 @@ def test_long_sequences(n, kind):
         check(c, keep, 4 if keep > 20 else 0, min(keep - 4, 300), what=f"{n} tokens, {kind}")
 
 
+def test_long_and_short_sequences_together():
+    """A table of 70000 tokens whose rows are filled by different amounts."""
+    for kind in ("heavy", "close", "odd"):
+        c = make([70000, 34001, 34000, 33999, 100, 1, 0], 3, 16, seed=9, positions=True, kind=kind)
+        for keep, sinks, recent in ((34000, 4, 500), (64, 0, 0), (1, 0, 1), (69999, 5, 0)):
+            check(c, keep, sinks, recent, what=f"long and short, {kind}")
+
+
+def test_long_rows_at_once_and_in_a_graph():
+    """A workspace for each of two streams; a graph replayed while lengths and weights change."""
+    c, d = make([40000, 33000], 2, 64, seed=1, positions=True), make([50000], 4, 64, seed=2, kind="ties")
+
+    def run(x, ws, keep=9000):
+        return nv.nvfp4_kv_select(x["w"], x["table"], x["kv_lens"], x["page"], keep, positions=x["pos"],
+                                  next_positions=x["nxt"], sinks=4, recent=300, ws=ws)
+
+    def room(x):
+        need = nv.nvfp4_workspace_size(nv._lib.OP_KV_SELECT, 0, 0, x["w"].shape[0], x["table"].shape[1] * x["page"],
+                                       x["table"].shape[0])
+        return torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+
+    want = [run(x, None) for x in (c, d)]
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [room(x) for x in (c, d)]
+    torch.cuda.synchronize()
+    step("two streams")
+    got = []
+    for _ in range(3):
+        for x, s, ws in zip((c, d), streams, spaces):
+            with torch.cuda.stream(s):
+                got.append(run(x, ws))
+    torch.cuda.synchronize()
+    for i, (moves, lens) in enumerate(got):
+        assert torch.equal(moves, want[i % 2][0]) and torch.equal(lens, want[i % 2][1]), i
+    graph = torch.cuda.CUDAGraph()
+    step("graph capture")
+    with torch.cuda.graph(graph):
+        moves, lens = run(c, spaces[0])
+    for rep, now in enumerate(([40000, 33000], [9000, 33000], [39999, 20], [0, 9001])):
+        c["kv_lens"].copy_(torch.tensor(now, dtype=torch.int32))
+        c["w"].copy_(c["w"].roll(77, 1))
+        eager = run(c, None)
+        torch.cuda.synchronize()
+        step(f"graph replay {rep}")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(moves, eager[0]) and torch.equal(lens, eager[1]), rep
+        held = chosen(c["w"], c["pos"], c["table"], c["kv_lens"], c["page"], 9000, c["nxt"], 4, 300, moves.shape[2])
+        np.testing.assert_array_equal(moves.cpu().numpy(), held[0])
+
+
 def test_one_more_token_than_the_budget():
     c = make([129] * 70, 8, 16, seed=3, positions=True)
     moves = check(c, 128, 4, 32)
