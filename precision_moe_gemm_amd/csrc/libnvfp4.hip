@@ -324,6 +324,10 @@ bool attention_rows_fit(const AttnArgs& a, int rows)
 // (14.5), 6000 tokens 38 (16); 32 sequences (256 workgroups) of 700 tokens 14.0
 // (17.5), 64 of them 24.9 (21.4).
 constexpr int64_t kWholeTiles = 256, kWholeTokens = 1024;
+bool attention_rows_whole(const AttnArgs& a, int rows)
+{
+    return attention_tiles(a, rows) * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens;
+}
 // Waves of the joining launch (four per SIMD).  4 sequences of 4000 tokens, 8 KV
 // heads of 128: 22 us together with the shares (24 with 8192 waves, 23 with
 // 16384); 8 sequences, 4 heads of 256: 32, 32, 35; 64 sequences: 70, 70, 72.
@@ -332,7 +336,7 @@ template <int D, int NT, bool TREE>
 nvfp4_status launch_attention_rows(AttnArgs a, hipStream_t st)
 {
     const int64_t tiles = attention_tiles(a, 16 * NT);
-    if (tiles * a.kv_heads <= kWholeTiles && (int64_t)a.pages * a.page <= kWholeTokens) {
+    if (attention_rows_whole(a, 16 * NT)) {
         a.whole = 1;
         a.head_lanes = 1;
         attn_rows_kernel<D, NT, TREE>
@@ -397,6 +401,10 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
     // and 239; one sequence 20 and 20.  With 32 KV heads and 64 prompts of 60 tokens 57 and 73, of 120 122 and
     // 112, 100 rows on 600 tokens of heads of 64 151 and 99.  Tiles of 16 rows for 32: 107 us where one of 32
     // takes 80, 64 sequences)
+    // Trees whose tiles of 16 rows are a workgroup each and leave CUs free: 16 drafts and 32/8 heads on 700 tokens 16.8 us,
+    // with tiles of 32 rows 22.4; four such trees 17.2 and 23.0
+    if (TREE && max_q * a.group <= 64 && attention_rows_whole(a, 16))
+        return launch_attention_rows<D, 1, TREE>(a, st);
     if (max_q * a.group <= 64 && attention_rows_fit(a, 32))
         return launch_attention_rows<D, 2, TREE>(a, st);
     // (128 rows of 64 sequences, 128-row tiles and 256-row ones: 239 and 257 us, heads of 64 72 and 85; 192 rows

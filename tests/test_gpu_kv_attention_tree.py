@@ -219,6 +219,44 @@ def test_many_sequences():
     check(make(m, kv, 1, 2, 64, 16, seed=9), "300 sequences")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("max_q", [40, 200])
+def test_tiles_of_many_sequences(D, max_q):
+    """Shares of the tile kernel that hold many tiles, of more sequences than a wave has lanes."""
+    r = np.random.default_rng(D)
+    m = [int(v) for v in r.integers(0, 40, 90)]
+    kv = [a + int(v) for a, v in zip(m, r.integers(0, 400, 90))]
+    check(make(m, kv, 1, 3, D, 16, seed=D), f"90 trees D={D} max_q={max_q}", max_q=max_q)
+    check(make(m[:20], kv[:20], 2, 9, D, 16, seed=D), f"20 trees, several tiles each, D={D}", max_q=max_q)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tiles_of_many_shares(D):
+    """A long context beside short ones: a tile that many workgroups share."""
+    c = make([33, 2, 40], [20000, 100, 3000], 1, 8, D, 64, seed=D)
+    check(c, f"long beside short D={D}")
+    check(c, f"long beside short D={D}, window", window=2500)
+
+
+@pytest.mark.parametrize("max_q", [4, 20, 70, 200])
+def test_many_heads(max_q):
+    check(make([3, 40], [90, 130], 268, 1, 64, 16, seed=4), f"268 KV heads max_q={max_q}", max_q=max_q)
+    check(make([3, 40], [90, 130], 515, 1, 64, 16, seed=4), f"515 KV heads max_q={max_q}", max_q=max_q)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_short_contexts_by_the_number_of_trees(D):
+    """Tables of up to 1024 tokens: tiles of 16 rows, of 32, and shares."""
+    for seqs in (1, 3, 8, 12):
+        kv = [100 + 61 * b for b in range(seqs)]
+        check(make([16] * seqs, kv, 8, 4, D, 16, seed=seqs), f"{seqs} trees of 16 D={D}")
+
+
+@pytest.mark.parametrize("max_q", [8, 20, 200])
+def test_the_widest_window(max_q):
+    check(make([9, 40], [90, 300], 2, 2, 128, 16, seed=37), f"window=2^31-1 max_q={max_q}", max_q=max_q, window=2 ** 31 - 1)
+
+
 def test_another_stream_graph_replays_and_a_workspace_each():
     """Two captured graphs with a workspace each, replayed while contexts and masks change."""
     c = make([9, 3, 20], [400, 90, 633], 2, 4, 128, 16, seed=81)
