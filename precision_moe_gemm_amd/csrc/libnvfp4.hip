@@ -400,23 +400,28 @@ nvfp4_status launch_attention(AttnArgs a, int64_t max_q, hipStream_t st)
 {
     a.head_lanes = attention_head_lanes(a.kv_heads);
     a.workers = attention_workers(a.kv_heads, a.head_lanes);
-    if (max_q * a.group <= 16 && attention_rows_fit(a, 16))
+    // (trees whose tiles of 16 rows are a workgroup each, of any number of rows: 16 drafts and 32/8 heads on 700 tokens
+    // 16.8 us, with tiles of 32 rows 22.4; 64 drafts on 900 20.2, with 256-row tiles 31.7; 4 heads of 256, 512 rows
+    // 27 and 39)
+    if ((max_q * a.group <= 16 && attention_rows_fit(a, 16)) || (TREE && attention_rows_whole(a, 16)))
         return launch_attention_rows<D, 1, TREE>(a, st);
     // (rows of a sequence and KV head, GPU time of row tiles of 32 and of tiles of 128 rows, 8 KV heads of 128,
     // 4000 tokens: 64 rows of 8 sequences 34 and 74 us, of 64 sequences 126 and 235; 128 rows of 64 sequences 245
     // and 239; one sequence 20 and 20.  With 32 KV heads and 64 prompts of 60 tokens 57 and 73, of 120 122 and
     // 112, 100 rows on 600 tokens of heads of 64 151 and 99.  Tiles of 16 rows for 32: 107 us where one of 32
     // takes 80, 64 sequences)
-    // Trees whose tiles of 16 rows are a workgroup each and leave CUs free: 16 drafts and 32/8 heads on 700 tokens 16.8 us,
-    // with tiles of 32 rows 22.4; four such trees 17.2 and 23.0
-    if (TREE && max_q * a.group <= 64 && attention_rows_whole(a, 16))
-        return launch_attention_rows<D, 1, TREE>(a, st);
     if (max_q * a.group <= 64 && attention_rows_fit(a, 32))
         return launch_attention_rows<D, 2, TREE>(a, st);
     // (128 rows of 64 sequences, 128-row tiles and 256-row ones: 239 and 257 us, heads of 64 72 and 85; 192 rows
     // 391 and 283, 107 and 89)
-    if (D == 256 || max_q * a.group <= 128)
+    // Trees of heads of 128: 256-row tiles, whose waves without rows only decode, also for fewer rows (128 rows of 64
+    // sequences of 4000 tokens 228 us, 128-row tiles 307, row tiles 299; of 8 sequences 50, 68, 54; heads of 64 152, 139,
+    // 201 and 38, 40, 41)
+    if constexpr (D == 256)
         return launch_attention_tiles<D, 4, TREE>(a, st);
+    else if constexpr (!TREE || D == 64)
+        if (max_q * a.group <= 128)
+            return launch_attention_tiles<D, 4, TREE>(a, st);
     if constexpr (D < 256)
         return launch_attention_tiles<D, 8, TREE>(a, st);
 }

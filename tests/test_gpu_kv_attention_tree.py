@@ -48,13 +48,23 @@ def reference(c, **kw):
                           c["mask"], **kw)
 
 
+def widened(c):
+    """The same sequences in rows of the table of more than 1024 tokens (which take other launches)."""
+    more = torch.full((c["table"].shape[0], -(-1025 // c["page"])), -1, dtype=torch.int32, device=DEV)
+    return dict(c, table=torch.cat([c["table"], more], 1))
+
+
 def check(c, what, max_q=None, **kw):
-    step(what)
-    out, lse = call(c, max_q, **kw)
-    torch.cuda.synchronize()
-    assert nv.nvfp4_get_error() == 0, what
-    assert_attention(out, lse, reference(c, **kw), what)
-    return out, lse
+    want = reference(c, **kw)
+    results = []
+    for x, table in ((c, "its own table"), (widened(c), "a wide table")):
+        step(f"{what}, {table}")
+        out, lse = call(x, max_q, **kw)
+        torch.cuda.synchronize()
+        assert nv.nvfp4_get_error() == 0, (what, table)
+        assert_attention(out, lse, want, f"{what}, {table}")
+        results.append((out, lse))
+    return results[0]
 
 
 # contexts that end inside and at the end of pages, of steps of 32 and of blocks of 64; trees of one word, of
@@ -149,10 +159,11 @@ def test_fewer_cached_tokens_than_drafts():
         check(c, f"more drafts than tokens, window={window}", window=window)
 
 
+@pytest.mark.parametrize("table", [dict, widened])
 @pytest.mark.parametrize("max_q", [2, 100])
-def test_too_few_words(max_q):
+def test_too_few_words(max_q, table):
     """Drafts behind the mask's words raise an error and are hidden."""
-    c = make([40, 20], [140, 60], 2, 2, 128, 16, seed=4)
+    c = table(make([40, 20], [140, 60], 2, 2, 128, 16, seed=4))
     bits = bits_of(c["mask"])[:, :32]
     c["mask"] = mask_of(bits).to(DEV)
     step("too few words")
@@ -167,25 +178,29 @@ def test_too_few_words(max_q):
     assert_attention(out, lse, reference(c), "no words")
 
 
-def test_bad_pages_and_pages_before_the_window():
-    c = make([6, 40], [300, 200], 2, 2, 64, 16, seed=8)
-    whole, _ = call(c, window=50)
+@pytest.mark.parametrize("table", [dict, widened])
+@pytest.mark.parametrize("max_q", [20, 40])
+def test_bad_pages_and_pages_before_the_window(max_q, table):
+    c = table(make([6, 40], [300, 200], 2, 2, 64, 16, seed=8))
+    whole, _ = call(c, max_q, window=50)
     c["table"][0, :(300 - 6 - 50) // 16] = -1
     c["table"][1, :(200 - 40 - 50) // 16] = 1 << 30
-    out, _ = check(c, "window with freed pages", window=50)
+    out, _ = check(c, "window with freed pages", max_q, window=50)
     assert torch.equal(whole, out)
-    c["table"][0, -1 if c["table"].shape[1] < 19 else 18] = -7  # the drafts' page
+    c["table"][0, 18] = -7  # the drafts' page
     step("bad page")
-    out, lse = call(c, window=50)
+    out, lse = call(c, max_q, window=50)
     torch.cuda.synchronize()
     assert nv.nvfp4_get_error() == 3
     assert_attention(out, lse, reference(c, window=50), "a bad page is skipped")
 
 
-def test_strided_rows_and_rows_behind_the_last_sequence():
-    c = make([3, 20], [40, 90], 2, 2, 128, 16, seed=17)
+@pytest.mark.parametrize("table", [dict, widened])
+@pytest.mark.parametrize("max_q", [20, 200])
+def test_strided_rows_and_rows_behind_the_last_sequence(max_q, table):
+    c = table(make([3, 20], [40, 90], 2, 2, 128, 16, seed=17))
     n, qh, D = c["q"].shape
-    plain, plain_lse = call(c)
+    plain, plain_lse = call(c, max_q)
     wide = torch.randn((n + 5, qh * D + 136), device=DEV).bfloat16()
     wide[:n, 8:8 + qh * D] = c["q"].reshape(n, -1)
     c["q"] = wide[:, 8:8 + qh * D].unflatten(1, (qh, D))
@@ -193,16 +208,17 @@ def test_strided_rows_and_rows_behind_the_last_sequence():
     outw = torch.full((n + 5, qh * D + 24), 7.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((n + 5, qh), 7.0, device=DEV)
     step("strided rows")
-    out, _ = call(c, out=outw[:, 16:16 + qh * D].unflatten(1, (qh, D)), lse=lse)
+    out, _ = call(c, max_q, out=outw[:, 16:16 + qh * D].unflatten(1, (qh, D)), lse=lse)
     torch.cuda.synchronize()
     assert torch.equal(out[:n], plain) and torch.equal(lse[:n], plain_lse)
     assert (outw[n:] == 7).all() and (lse[n:] == 7).all()
     assert (outw[:, :16] == 7).all() and (outw[:, 16 + qh * D:] == 7).all()
 
 
+@pytest.mark.parametrize("table", [dict, widened])
 @pytest.mark.parametrize("max_q", [4, 60])
-def test_a_row_of_nan_spoils_itself_alone(max_q):
-    c = make([20, 9], [90, 400], 2, 2, 128, 16, seed=23)
+def test_a_row_of_nan_spoils_itself_alone(max_q, table):
+    c = table(make([20, 9], [90, 400], 2, 2, 128, 16, seed=23))
     want, want_lse = call(c, max_q)
     c["q"][5, 1, 7] = float("nan")
     out, lse = call(c, max_q)
@@ -257,9 +273,10 @@ def test_the_widest_window(max_q):
     check(make([9, 40], [90, 300], 2, 2, 128, 16, seed=37), f"window=2^31-1 max_q={max_q}", max_q=max_q, window=2 ** 31 - 1)
 
 
-def test_another_stream_graph_replays_and_a_workspace_each():
+@pytest.mark.parametrize("table", [dict, widened])
+def test_another_stream_graph_replays_and_a_workspace_each(table):
     """Two captured graphs with a workspace each, replayed while contexts and masks change."""
-    c = make([9, 3, 20], [400, 90, 633], 2, 4, 128, 16, seed=81)
+    c = table(make([9, 3, 20], [400, 90, 633], 2, 4, 128, 16, seed=81))
     full, bits = c["kv_lens"].clone(), bits_of(c["mask"])
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
