@@ -618,7 +618,7 @@ def _kv_attention(q, k_cache, v_cache, heads, block_table, kv_lens, page_size, c
         if n > 1 and mask.stride(0) < mask.shape[1]:
             raise ValueError("mask: rows must not overlap")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     ld_out = _heads(out, "out", device)
     if out.shape != q.shape:
         raise ValueError("out: the shape of q is expected")
