@@ -454,7 +454,12 @@ void set_pages(AttnArgs& a, const int32_t* block_table, int64_t ld_table, int32_
 }
 
 // ---------------------------------------------------------------- eviction
-// Query rows of a sequence and KV head up to which weights go by the row kernel.
+// Query rows of a sequence and KV head up to which weights go by the row kernel
+// (tiles of 16 rows, of 32 and of 64).  Us by rows and by tiles, 16 sequences of 8000
+// tokens, 4 KV heads: 64 rows 35 and 48 (D = 128), 29 and 37 (64), 59 and 81
+// (256); 4 sequences of 1000 tokens 20 and 25, 18 and 22, 29 and 23; 128 rows,
+// walked twice, 57 and 57, 47 and 46, 99 and 96, and 28 and 25, 24 and 23, 45
+// and 24.
 constexpr int64_t kWeighFew = 64;
 
 // The row kernel counts its steps in 31 bits; what does not fit goes to the
