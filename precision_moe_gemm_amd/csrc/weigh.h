@@ -56,8 +56,10 @@ NVFP4_DEV void weigh_shifts(const float* src, float4_t (&z)[4])
         : "memory");
 }
 
-// The tokens whose weights a call writes: all of a sequence's, without those
-// before every window where they are in place.
+// The first token whose weight a call writes: in place, the first in the first
+// row's window (entries of pages that lie wholly before it may hold anything,
+// another sequence's page as well).  Steps and blocks begin before it, at
+// whole multiples of their tokens; what they store does not.
 NVFP4_DEV int weigh_first(const WeighArgs& w, const AttnSeq& s)
 {
     int lo, hi;
@@ -229,7 +231,7 @@ weigh_rows_kernel(WeighArgs w)
     float* sums = run[wave];
     while (u < u1) {
         const AttnSeq s = attn_seq_uniform(a, own, f.seq);
-        const int first = weigh_first(w, s) & ~(kAttnStep - 1);
+        const int lowest = weigh_first(w, s), first = lowest & ~(kAttnStep - 1);
         const int units = s.kv > first ? (s.kv - first + kAttnStep - 1) / kAttnStep : 0;
         if (f.at >= units) {
             f.seq++;
@@ -267,7 +269,8 @@ weigh_rows_kernel(WeighArgs w)
             }
             wait_lgkm0();
             for (int t = from + (int)(threadIdx.x & 63); t < end; t += 64)
-                weigh_put(w, row, h, t, fresh, sums[t - from]);
+                if (t >= lowest)
+                    weigh_put(w, row, h, t, fresh, sums[t - from]);
             wait_lgkm0();
         }
         u += n;
@@ -390,7 +393,7 @@ weigh_tile_kernel(WeighArgs w)
         const int64_t in_seq = job - (int64_t)f.before.units * splits;
         const int h = (int)(in_seq % a.kv_heads);
         const int split = (int)(in_seq / a.kv_heads % splits), block = (int)(in_seq / a.kv_heads / splits);
-        const int t0 = (weigh_first(w, s) / BT + block) * BT;
+        const int lowest = weigh_first(w, s), t0 = (lowest / BT + block) * BT;
         const int32_t* table = a.table + f.seq * a.ld_table;
         int r0, r1;
         weigh_span(a, s, t0, t0 + BT < s.kv ? t0 + BT : s.kv, &r0, &r1);
@@ -607,7 +610,7 @@ weigh_tile_kernel(WeighArgs w)
         }
         wait_vm<0>();
         sum += __shfl_xor(sum, 32, 64);
-        if (e == 0 && token < s.kv) {
+        if (e == 0 && token >= lowest && token < s.kv) {
             if (splits > 1) {
                 // [sequence's units in a row: block, head][split][token of the block]
                 const int64_t unit = f.before.units + (int64_t)block * a.kv_heads + h;
@@ -638,8 +641,9 @@ weigh_join_kernel(WeighArgs w)
     for (int unit = blockIdx.x; unit < scan.units; unit += gridDim.x) {
         const AttnFound f = attn_find(scan, a.seqs, unit, count);
         const AttnSeq s = attn_seq_uniform(a, own, f.seq);
-        const int h = f.at % a.kv_heads, t = (weigh_first(w, s) / BT + f.at / a.kv_heads) * BT + (int)threadIdx.x;
-        if (t >= s.kv)
+        const int lowest = weigh_first(w, s);
+        const int h = f.at % a.kv_heads, t = (lowest / BT + f.at / a.kv_heads) * BT + (int)threadIdx.x;
+        if (t < lowest || t >= s.kv)
             continue;
         float sum = 0.0f;
         for (int i = 0; i < splits; i++)
