@@ -627,13 +627,13 @@ nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n
  *   weights_out: the same shape, row stride ld_out; it may be w itself with the
  *   same stride (one that shares an element with w otherwise:
  *   NVFP4_ERR_INVALID_ARG).  Written are the cached tokens of the call's sequences
- *   only; in place, tokens before every row's window are left as they are, and
- *   entries of pages that lie wholly before it may hold anything (pages that
- *   other sequences have by now among them).  Elsewhere those tokens are copied,
- *   and their entries are needed: a sequence that gave pages up is weighed in
- *   place.
- *   max_q: as there (a wrong one costs speed, not results).  With n = 0 (q and lse
- *   may be NULL) the weights are copied.
+ *   only; in place, tokens before every row's window and sequences without rows
+ *   are left as they are, and entries of pages that hold no other token may hold
+ *   anything (pages that other sequences have by now among them).  Elsewhere
+ *   those tokens are copied, and their entries are needed: a sequence that gave
+ *   pages up is weighed in place.
+ *   max_q: as there (a wrong one costs speed, not results).  With n = 0 q and lse
+ *   may be NULL.
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs)
  *   bytes, 256-byte aligned.
  * Each of the weights counts as a number of [0, 1], a NaN as 0: rows of q with a

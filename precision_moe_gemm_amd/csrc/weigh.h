@@ -58,13 +58,20 @@ NVFP4_DEV void weigh_shifts(const float* src, float4_t (&z)[4])
 
 // The first token whose weight a call writes: in place, the first in the first
 // row's window (entries of pages that lie wholly before it may hold anything,
-// another sequence's page as well).  Steps and blocks begin before it, at
-// whole multiples of their tokens; what they store does not.
+// another sequence's page as well), and none of a sequence without rows.  Steps
+// and blocks begin before it, at whole multiples of their tokens; what they
+// store does not.
 NVFP4_DEV int weigh_first(const WeighArgs& w, const AttnSeq& s)
 {
     int lo, hi;
     attn_limits(w.a, s, 0, &lo, &hi);
-    return w.before == w.after && s.nq > 0 ? lo : 0;
+    return w.before != w.after ? 0 : (s.nq > 0 ? lo : s.kv);
+}
+
+// The steps or blocks of `each` tokens that hold the tokens from `first` on.
+NVFP4_DEV int weigh_units(int first, int kv, int each)
+{
+    return first < kv ? (kv + each - 1) / each - first / each : 0;
 }
 
 // Adds x to what token t of a sequence and KV head had (from `fresh` on: nothing).
@@ -217,8 +224,7 @@ weigh_rows_kernel(WeighArgs w)
     AttnSeq own{0, 0, 0, false};
     auto count = [&](int b) {
         own = attn_seq(a, b);
-        const int t0 = weigh_first(w, own) & ~(kAttnStep - 1);
-        return AttnCount{1, own.kv > t0 ? (own.kv - t0 + kAttnStep - 1) / kAttnStep : 0, own.down};
+        return AttnCount{1, weigh_units(weigh_first(w, own), own.kv, kAttnStep), own.down};
     };
     const AttnScan scan = attn_scan(a.seqs, count);
     const int64_t total = scan.units;
@@ -232,7 +238,7 @@ weigh_rows_kernel(WeighArgs w)
     while (u < u1) {
         const AttnSeq s = attn_seq_uniform(a, own, f.seq);
         const int lowest = weigh_first(w, s), first = lowest & ~(kAttnStep - 1);
-        const int units = s.kv > first ? (s.kv - first + kAttnStep - 1) / kAttnStep : 0;
+        const int units = weigh_units(lowest, s.kv, kAttnStep);
         if (f.at >= units) {
             f.seq++;
             f.at = 0;
@@ -323,10 +329,9 @@ constexpr int kWeighJobs = 1024;    // parts of split blocks, at most
 template <int D>
 NVFP4_DEV AttnCount weigh_count(const WeighArgs& w, const AttnSeq& s)
 {
-    const int t0 = weigh_first(w, s) / weigh_block<D>() * weigh_block<D>();
     AttnCount c;
     c.tiles = w.a.kv_heads;
-    c.units = s.kv > t0 ? (s.kv - t0 + weigh_block<D>() - 1) / weigh_block<D>() : 0;
+    c.units = weigh_units(weigh_first(w, s), s.kv, weigh_block<D>());
     c.down = s.down;
     return c;
 }

@@ -69,6 +69,37 @@ def test_pages_given_up_before_the_window(D, heads, group, page, max_q):
         assert torch.equal(bits(got), bits(want)), (kind, what)
 
 
+@pytest.mark.parametrize("max_q", [1, 16, 32, 200])
+@pytest.mark.parametrize("window", [0, 40])
+def test_sequences_without_rows_are_left_alone(window, max_q):
+    """Idle slots, whose rows of the table may hold anything, beside others and with no other."""
+    for q, kv in (([0, 3, 0, 0, 1], [200, 90, 33, 64, 300]), ([0, 0], [95, 600])):
+        c = make(q, kv, 2, 2, 128, 16, seed=6)
+        with_lse(c, window=window) if sum(q) else c.update(lse=torch.empty((0, 4), device=DEV))
+        idle = [b for b in range(len(q)) if q[b] == 0]
+        for b in idle:
+            c["before"][:, places(c, b, 0, kv[b])] = -0.0
+        what = f"idle slots {idle}, window={window} max_q={max_q}"
+        step(what)
+        want = in_place(c, c["table"], max_q, window=window)
+        assert nv.nvfp4_get_error() == 0, what
+        ref = list(received(c["q"], c["lse"], c["k_cache"], 2, c["table"], c["kv_lens"], 16, c["before"], cu_q=c["cu_q"],
+                            window=window))
+        for b in idle:
+            ref[2][:, places(c, b, 0, kv[b]).cpu()] = False
+        agree(want, ref, c["before"], what)
+        assert torch.equal(bits(want)[~ref[2].to(DEV)], bits(c["before"])[~ref[2].to(DEV)]), what
+        for entry in (-1, 1 << 24, "another's"):
+            table = c["table"].clone()
+            for b in idle:
+                other = c["table"][(b + 1) % len(q)]
+                table[b] = other.clamp(min=0) if entry == "another's" else entry
+            step(f"{what}, entries {entry}")
+            got = in_place(c, table, max_q, window=window)
+            assert nv.nvfp4_get_error() == 0, (entry, what)
+            assert torch.equal(bits(got), bits(want)), (entry, what)
+
+
 @pytest.mark.parametrize("max_q", [1, 200])
 def test_a_bad_page_in_the_window_is_reported(max_q):
     c = with_lse(make([1, 3], [300, 200], 2, 2, 64, 16, seed=3), window=40)
