@@ -636,15 +636,16 @@ nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n
  *   may be NULL.
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs)
  *   bytes, 256-byte aligned.
- * Each of the weights counts as a number of [0, 1], a NaN as 0: rows of q with a
- * NaN or infinity and rows with an lse that is not finite add nothing.  The order
- * of a token's sum is set by the arguments: no atomics.  Scores past fp32's range
- * (in units of ln 2) count as 0 or 1.  A page must belong to one sequence of the
- * call; tokens of a page that two of them hold get the sum of either.  Lengths,
- * offsets and entries that are out of range are handled as in
- * nvfp4_kv_attention.  D is 64, 128 or 256 (scales 16-byte aligned with 256),
- * page_size % 16 == 0, a row of the table covers at most 2^30 tokens on this
- * build.
+ * Each of the weights counts as a number of [0, 1].  Rows with an lse that is not
+ * finite add nothing; nvfp4_kv_attention returns such a one for a row of q with
+ * a NaN or infinity.  Under a finite lse from elsewhere a score that is NaN
+ * counts as 0, and an infinite one, as any past fp32's range (in units of ln 2),
+ * as 0 or 1 by its sign.  The order of a token's sum is set by the arguments: no
+ * atomics.  A page must belong to one sequence of the call; tokens of a page that
+ * two of them hold get the sum of either.  Lengths, offsets and entries that are
+ * out of range are handled as in nvfp4_kv_attention.  D is 64, 128 or 256 (scales
+ * 16-byte aligned with 256), page_size % 16 == 0, a row of the table covers at
+ * most 2^30 tokens on this build.
  */
 nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32_t q_heads, const float* lse,
                               const nvfp4_tensor* k_cache, int32_t kv_heads, const int32_t* block_table,

@@ -11,7 +11,10 @@
 // its rows, by a fixed number of them in a fixed order): results do not depend
 // on the order of the waves.  A weight is held to [0, 1], which the clamp of
 // the exponential's result gives for nothing; the clamp also makes a NaN a
-// zero, so rows with a NaN, an infinity or no lse add nothing.
+// zero.  A row whose lse is not finite adds nothing, and a row of q with a NaN
+// or an infinity has no finite one: its scores are NaN or infinite throughout.
+// (Under a finite lse from elsewhere an infinite score is 0 or 1; a test for it
+// would read all of q once more.)
 //
 // S = Q K^T with a token per column: a lane holds the scores of one token for
 // several rows, and the sum over the rows stays within the lane until the last
