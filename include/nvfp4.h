@@ -701,7 +701,8 @@ nvfp4_status nvfp4_kv_select(const float* weights, int64_t ld_weights, const int
  * place's content is that of any of them.  A place outside the table or in an
  * entry that is not a page of the cache raises the sticky NVFP4_ERR_RANGE, and
  * the pair moves nothing.  Pages that are moved within must belong to one
- * sequence of the call.  D % 32 == 0 and D <= 4096 on this build.
+ * sequence of the call.  K and V may be one tensor, which is then moved once;
+ * otherwise they share no memory (else NVFP4_ERR_INVALID_ARG).  D % 32 == 0 and D <= 4096 on this build.
  */
 nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_cache, int32_t kv_heads,
                            const int32_t* block_table, int64_t ld_table, int32_t pages_per_seq, int32_t page_size,

@@ -628,8 +628,9 @@ select_moves_kernel(SelectArgs s)
 // ---------------------------------------------------------------------------
 struct MoveArgs {
     AttnArgs a;           // table, pages, kv_heads
-    uint8_t* codes[2];    // K, V
+    uint8_t* codes[2];    // K, V (one where both lie in the same memory: tensors = 1)
     uint8_t* scales[2];
+    int tensors;
     int dim;
     int scale_unit;       // bytes: 16, 8, 4 or 2
     int code_units, scale_units, units;  // of one tensor, of one tensor, in all
@@ -648,18 +649,18 @@ typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
 NVFP4_DEV uint8_t* move_at(const MoveArgs& m, int u, int64_t token, int h, int* bytes)
 {
     const int64_t row = token * m.a.kv_heads + h;
-    if (u < 2 * m.code_units) {
+    if (u < m.tensors * m.code_units) {
         const int which = u >= m.code_units;
         *bytes = 16;
         return (which ? m.codes[1] : m.codes[0]) + row * (m.dim / 2) + (u - which * m.code_units) * 16;
     }
-    u -= 2 * m.code_units;
-    if (u < 2 * m.scale_units) {
+    u -= m.tensors * m.code_units;
+    if (u < m.tensors * m.scale_units) {
         const int which = u >= m.scale_units;
         *bytes = m.scale_unit;
         return (which ? m.scales[1] : m.scales[0]) + row * (m.dim / 16) + (u - which * m.scale_units) * m.scale_unit;
     }
-    u -= 2 * m.scale_units;
+    u -= m.tensors * m.scale_units;
     *bytes = 4;
     return u == 0 && m.weights ? (uint8_t*)(m.weights + h * m.ld_w + token) : (uint8_t*)(m.positions + h * m.ld_pos + token);
 }

@@ -2762,7 +2762,16 @@ nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_ca
         return st;
     if (seqs == 0 || cap == 0 || pages_per_seq == 0)
         return NVFP4_OK;
-    if (D == 0 || D % 32 != 0 || D > 4096 || cap > 0x3FFFFFFF)
+    if (D == 0 || D % 32 != 0 || D > 4096)
+        return NVFP4_ERR_UNSUPPORTED;
+    // One tensor as both is moved once: each unit of a row is read and written by one wave, and a second one would
+    // find sources that the first has written.
+    const bool one = k_cache->packed == v_cache->packed && k_cache->scales == v_cache->scales;
+    const int64_t codes = k_cache->rows * (D / 2), scales = k_cache->rows * (D / 16);  // bytes
+    if (!one && (rows_share(k_cache->packed, codes, codes, v_cache->packed, codes, codes, 1, 1) ||
+                 rows_share(k_cache->scales, scales, scales, v_cache->scales, scales, scales, 1, 1)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (cap > 0x3FFFFFFF)
         return NVFP4_ERR_UNSUPPORTED;
     if ((weights && ld_weights < tokens) || (positions && ld_positions < tokens))
         return NVFP4_ERR_SHAPE;
@@ -2775,11 +2784,12 @@ nvfp4_status nvfp4_kv_move(const nvfp4_tensor* k_cache, const nvfp4_tensor* v_ca
         m.codes[j] = cache[j]->packed;
         m.scales[j] = cache[j]->scales;
     }
+    m.tensors = one ? 1 : 2;
     m.dim = (int)D;
     m.scale_unit = D % 256 == 0 ? 16 : (D % 128 == 0 ? 8 : (D % 64 == 0 ? 4 : 2));
     m.code_units = (int)(D / 32);
     m.scale_units = (int)(D / 16 / m.scale_unit);
-    m.units = 2 * (m.code_units + m.scale_units) + (weights != nullptr) + (positions != nullptr);
+    m.units = m.tensors * (m.code_units + m.scale_units) + (weights != nullptr) + (positions != nullptr);
     m.weights = weights;
     m.ld_w = ld_weights;
     m.positions = positions;

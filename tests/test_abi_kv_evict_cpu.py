@@ -236,6 +236,25 @@ def test_move_refusals(lib):
     assert move(lib, pos=P(66)) == L.INVALID_ARG
 
 
+def test_move_of_caches_that_share_memory(lib):
+    """K and V are one tensor, or lie apart: 64 rows of 64 bytes of codes and 8 of scales."""
+    from precision_moe_gemm_amd import _lib as L
+    k, s = 1 << 20, 1 << 21
+
+    def refused(packed, scales):
+        kc, vc = cache(packed=k, scales=s), cache(packed=packed, scales=scales)
+        got = move(lib, kc=kc, vc=vc, cap=1 << 30)                  # (stops what is not refused before a launch)
+        assert got in (L.INVALID_ARG, L.UNSUPPORTED) and got == move(lib, kc=vc, vc=kc, cap=1 << 30)
+        return got == L.INVALID_ARG
+
+    assert not refused(k, s)
+    for packed, scales in ((4096, 512), (-4096, -512), (4096, -512), (8192, 4096)):
+        assert not refused(k + packed, s + scales), (packed, scales)
+    for packed, scales in ((4096, 0), (0, 512), (16, 512), (4080, 512), (-4080, 512), (4096, 4), (4096, 508), (4096, -508),
+                           (16, 4)):
+        assert refused(k + packed, s + scales), (packed, scales)
+
+
 @pytest.mark.skipif("NVFP4_LIB_PATH" in os.environ, reason="this run is the sanitized one")
 def test_refusals_under_asan_ubsan():
     from precision_moe_gemm_amd import build

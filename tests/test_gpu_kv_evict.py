@@ -288,6 +288,22 @@ def test_nothing_to_move():
     check_move(state, table, 16, 2, np.array([[[[5, 5]]]], dtype=np.int32), "a token to itself")
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("cap", [5, 40, 200, 300])
+def test_one_tensor_as_keys_and_values(D, cap):
+    """It is moved once: chains up to 256 moves, else sources that nobody writes."""
+    heads, page, pool = 2, 16, 44
+    table = torch.randperm(pool, generator=torch.Generator().manual_seed(cap))[:40].view(1, 40).int().to(DEV)
+    r = np.random.default_rng(cap)
+    moves = np.full((1, heads, cap, 2), -1, dtype=np.int32)
+    for h in range(heads):
+        at = r.permutation(640)
+        moves[0, h, :, 0] = at[:cap]
+        moves[0, h, :, 1] = np.roll(at[:cap], 1) if cap <= 256 else at[cap:2 * cap]
+    kc, _, w, p = cache(pool, page, heads, D, cap)
+    check_move((kc, kc, w, p), table, page, heads, moves, f"K as V, D={D} cap={cap}")
+
+
 def test_strided_weights():
     kc, vc, w, p = cache(4, 16, 2, 64, 5)
     wide = torch.full((2, 64 + 9), 7.0, device=DEV)
