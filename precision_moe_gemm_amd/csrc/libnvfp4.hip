@@ -367,7 +367,7 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
     const int64_t tiles = attention_tiles(a.n, a.group, a.seqs, ROWS);  // (the workspace's count: it sets the splits)
     if (tiles * a.kv_heads * 64 * NW > 0xFFFFFFFF)  // threads of one dimension of a launch
         return NVFP4_ERR_UNSUPPORTED;
-    if (TREE) {
+    if constexpr (TREE) {
         AttnArgs b = a;
         b.workers = attention_tile_workers<D, NW>(a.kv_heads);
         if (tiles * (ceil_div((int64_t)a.pages * a.page, kTileTok) + kTileStart) > 0x7FFFFFFF)
