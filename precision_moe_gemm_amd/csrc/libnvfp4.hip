@@ -299,11 +299,12 @@ size_t attention_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64
 
 size_t attention_tree_ws_bytes(int64_t n, int q_heads, int kv_heads, int64_t D, int64_t seqs)
 {
-    // row kernel: as without trees; tile kernel: two slots per share, its rows of D + 4 values
+    // row kernel: as without trees; tile kernel: two slots per share, its rows (128, and up to D = 128 also 256) of D + 4
+    // values
     const int hl = attention_head_lanes(kv_heads);
     const size_t rows = (size_t)attention_workers(kv_heads, hl) * kv_heads * 2 * (D / 4 + 2) * 2 * 64 * sizeof(float);
     size_t part = rows;
-    for (int w = 128; w <= 256; w *= 2) {
+    for (int w = 128; w <= (D == 256 ? 128 : 256); w *= 2) {
         const int64_t workers = std::max(1, (w == 256 || D == 256 ? 256 : 512) / kv_heads);
         part = std::max(part, (size_t)(workers * kv_heads * 2 * w * (D + 4)) * sizeof(float));
     }

@@ -50,6 +50,16 @@ def test_tree_refusals(lib):
         assert tree(lib, **{name: None}) == L.INVALID_ARG, name
 
 
+def test_tree_workspace(lib):
+    """Two slots of the tile kernel's 256 workgroups for heads of 256: their 128 rows of 260 numbers (the row
+    kernel's slots take 264, the list of tiles a few KB)."""
+    from precision_moe_gemm_amd import _lib as L
+    for heads in (1, 4, 8):
+        need = lib.nvfp4_workspace_size(L.OP_KV_ATTENTION_TREE, 64, 8 * heads, heads, 256, 1)
+        slots = 256 * 2 * 128 * 260 * 4
+        assert slots <= need < slots * 1.02, heads
+
+
 WEIGHTS = dict(q=P(4096), ld_q=512, n=3, q_heads=4, lse=P(64), kc=None, heads=2, table=P(64), ld_table=2, pages=2, page=16,
                lens=P(64), cu=None, seqs=3, max_q=1, scale=0.1, causal=1, window=0, w=P(1 << 14), ld_w=32, out=P(1 << 15),
                ld_out=32, ws=P(1 << 20), ws_bytes=None)
