@@ -635,7 +635,7 @@ nvfp4_status nvfp4_kv_attention_tree(const void* q_bf16, int64_t ld_q, int64_t n
  *   max_q: as there (a wrong one costs speed, not results).  With n = 0 q and lse
  *   may be NULL.
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_WEIGHTS, n, q_heads, kv_heads, D, seqs)
- *   bytes, 256-byte aligned.
+ *   bytes, 256-byte aligned; calls that may overlap in time need one each.
  * Each of the weights counts as a number of [0, 1].  Rows with an lse that is not
  * finite add nothing; nvfp4_kv_attention returns such a one for a row of q with
  * a NaN or infinity.  Under a finite lse from elsewhere a score that is NaN
@@ -658,11 +658,12 @@ nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32
  * Which cached tokens each KV head of a sequence keeps when the sequence passes
  * its budget, as the moves that close the gaps (for nvfp4_kv_move).  A sequence
  * of at most `keep` tokens keeps them all.  Of a longer one, each KV head keeps
- * `keep`: first those at a position below `sinks` or among the last `recent`
- * before next_positions[b], then those with the largest weights; of equals (of
- * tokens kept first, should there be too many, as well) the ones at the lowest
- * place.  A NaN weight counts as -inf.  The i-th kept token at a place >= keep
- * (in the order of the places) moves to the i-th place < keep whose token goes.
+ * `keep`: first those at a position below `sinks` or from next_positions[b] -
+ * recent on (any past the newest among them), then those with the largest
+ * weights; of equals (of tokens kept first, should there be too many, as well) the
+ * ones at the lowest place.  A NaN weight counts as -inf.  The i-th kept token at
+ * a place >= keep (in the order of the places) moves to the i-th place < keep
+ * whose token goes.
  *   weights: fp32 [kv_heads, tokens], row stride ld_weights, as from
  *   nvfp4_kv_weights; positions: int32, the same shape, row stride ld_positions,
  *   each token's position in its sequence (moves mix the places), with
@@ -674,7 +675,8 @@ nvfp4_status nvfp4_kv_weights(const void* q_bf16, int64_t ld_q, int64_t n, int32
  *   lens_out: int32 [seqs], min(kv_lens[b], keep); neither kv_lens nor next_positions;
  *   ws: nvfp4_workspace_size(NVFP4_OP_KV_SELECT, 0, 0, kv_heads, pages_per_seq *
  *   page_size, seqs) bytes, 256-byte aligned (may be NULL if that is 0, as it is
- *   for rows of the table of up to 32768 tokens).
+ *   for rows of the table of up to 32768 tokens); calls that may overlap in time
+ *   need one each.
  * Nothing is moved, and weights are not changed.  keep >= 1, sinks + recent <=
  * keep (else NVFP4_ERR_INVALID_ARG).  A kv_lens[b] outside the table's places is
  * cut and raises the sticky NVFP4_ERR_RANGE, as does an entry that is not a page

@@ -695,7 +695,8 @@ def nvfp4_kv_weights(q: torch.Tensor, lse: torch.Tensor, k_cache: NVFP4Tensor, h
                      causal: bool = True, window: int = 0, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Add the attention weight that each cached token receives from q (bf16 [n,
     q_heads, D]) to weights (float32 [heads, cache tokens]; None: zeros) and write
-    it to out (the same shape; may be weights).  lse: what nvfp4_kv_attention
+    it to out (the same shape; may be weights, and must be for sequences that gave
+    up pages before their window).  lse: what nvfp4_kv_attention
     returned for these rows, whose arguments the others are."""
     device = q.device
     ld_q = _heads(q, "q", device)
@@ -738,8 +739,8 @@ def nvfp4_kv_select(weights: torch.Tensor, block_table: torch.Tensor, kv_lens: t
     """(moves, lens): the moves (int32 [seqs, heads, cap, 2], pairs of places, -1
     behind the last) after which each KV head of a sequence of more than `keep`
     tokens has the tokens that it keeps at its first `keep` places, and the lengths
-    afterwards (int32 [seqs]).  Kept are the tokens at positions below sinks, the
-    `recent` ones before next_positions (int32 [seqs]) and the heaviest of
+    afterwards (int32 [seqs]).  Kept are the tokens at positions below sinks,
+    those from next_positions (int32 [seqs]) - recent on and the heaviest of
     weights (float32 [heads, cache tokens]).  positions: int32, the shape of
     weights; None: places are positions.  cap: the most moves of a list (what the
     table's width can need if omitted)."""

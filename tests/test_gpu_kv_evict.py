@@ -155,6 +155,14 @@ def test_more_protected_tokens_than_places():
     check(c, 50, 0, 50)
 
 
+@pytest.mark.parametrize("n", [300, 34000])
+def test_positions_past_the_newest_count_as_recent(n):
+    c = make([n], 2, 16, seed=13, positions=True)
+    c["nxt"].fill_(2 * n)  # (positions reach 3 n)
+    for recent in (0, 1, 30):
+        check(c, n // 2, 0, recent, what="positions past the newest")
+
+
 def test_strides_and_a_roomy_list():
     c = make([300, 40], 2, 16, seed=7, positions=True)
     wide = torch.full((2, c["w"].shape[1] + 9), float("nan"), device=DEV)
