@@ -1078,9 +1078,10 @@ constexpr int kTileTok = 64;
 
 // TREE: the work of each of a sequence's tiles, in blocks of tokens, and the shares that the work of all tiles is
 // cut into.  Starting and ending a tile counts as kTileStart blocks, which come first, so that shares of many
-// short tiles take no longer than those of a long one (32 trees of 26-63 drafts on 300-16000 tokens 231 us with two,
-// 220 with four, 222 with eight; 4 trees of 60 on 2000 tokens, 4 KV heads of 256: 56, 58, 60).  A split of each
-// tile's blocks into as many parts as fill the chip took 421 us for the first, equal pieces of tiles 251.
+// short tiles take no longer than those of a long one (32 trees of 26-63 drafts on 300-16000 tokens, replayed: 213 us
+// with two, 201 with four, 200 with eight; 4 trees of 60 on 2000 tokens, 4 KV heads of 256: 58, 57, 59; one of 60 on
+// 3000, 8 heads of 128: 36, 36, 38).  Before waves without rows were left out a split of each tile's blocks into as
+// many parts as fill the chip took 421 us for the first, equal pieces of tiles 251 and these shares 220.
 constexpr int kTileStart = 4;
 NVFP4_DEV int attn_tile_units(const AttnArgs& a, const AttnSeq& s)
 {

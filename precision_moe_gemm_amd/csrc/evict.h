@@ -342,7 +342,7 @@ select_kernel(SelectArgs s)
 
 // ---- longer rows: shares of a list's tokens by workgroups of their own (one workgroup reads what others wrote
 // at 50 GB/s: five passes over 131072 keys took it 107 us), in four launches.  16384 of 131072 tokens, 4 KV heads:
-// 4.8 + 6.8 + 7.2 + 5.4 us, each little more than a launch and its chain of reads (342 by one workgroup a head with
+// 4.8 + 6.5 + 7.6 + 6.0 us, each little more than a launch and its chain of reads (342 by one workgroup a head with
 // sums across workgroups in between).  blockIdx.x: list, blockIdx.y: share.
 constexpr int kSelectThreads = 512;
 constexpr int kSelectSpan = 4096;   // tokens of a share, at least

@@ -377,9 +377,9 @@ nvfp4_status launch_attention_tiles(const AttnArgs& a, hipStream_t st)
         nvfp4_status s = launch_status();
         if (s != NVFP4_OK)
             return s;
-        // rows of a wave of the joining launch: one, or up to four where there are many tiles (one sequence of 60 drafts
-        // and 3000 tokens 35.1 us with one and 38.7 with four, 24 trees under a window 51.2 and 53.2; 64 trees of 60 on
-        // 300 tokens 85.5 and 76.2)
+        // rows of a wave of the joining launch: one, or up to four where there are many tiles (replayed, with one and
+        // with four: one sequence of 60 drafts and 3000 tokens 35.7 and 39.3 us, 24 trees under a window 51.4 and 52.2;
+        // 64 trees of 60 on 300 tokens 80.0 and 71.7)
         int rows = 1;
         while (rows < 4 && tiles * a.kv_heads * (ROWS / 4 / rows) > 8192)
             rows *= 2;
@@ -525,6 +525,10 @@ SelectLayout select_layout(int64_t lists, int64_t places)
     return y;
 }
 
+// One launch while the keys of a row of the table fit the shared memory, since the lengths are on the device.  One
+// launch of 1024 threads a list and four launches, replayed, 8 KV heads of 1, 16, 64 sequences: 8192 tokens 18 and 25,
+// 19 and 26, 31 and 44 us; 16384 tokens 23 and 24, 23 and 28, 41 and 60; 32768 tokens 33 and 24, 34 and 36, 62 and 91;
+// 2112 tokens in rows for 32768 20 and 23, 20 and 25, 25 and 46 (in rows for 131072 the four take 25, 41 and 46).
 nvfp4_status launch_select(SelectArgs s, uint8_t* ws, hipStream_t st)
 {
     const int64_t lists = (int64_t)s.a.seqs * s.a.kv_heads, places = (int64_t)s.a.pages * s.a.page;

@@ -99,10 +99,15 @@ NVFP4_DEV void weigh_put(const WeighArgs& w, const int32_t* table_row, int h, in
 // of up to kWeighRun tokens stay in shared memory and go to the weights in
 // runs of neighbours.
 //
-// 64 single tokens on 64-16384 tokens, 32/8 heads of 128: 40 us for 117 MB (2.9
+// 64 single tokens on 64-16384 tokens, 32/8 heads of 128: 42 us for 117 MB (2.8
 // TB/s; 23.5 us at the rate of a copy): the decode of K and the exponentials of
-// tiles that four rows fill of 16.  One sequence of 700 tokens: 8.6 us of
-// dependent reads (lengths, page, K, the weights before).
+// tiles that four rows fill of 16 (the vector unit works 64% of the cycles, the
+// matrix unit 8%).  64 rows of 16 x 8000 tokens, 4 heads of 64, 128, 256: 25, 31
+// and 55 us, 4.6, 8.4 and 16 at that rate: about eight steps a wave, whose waits
+// (43, 43 and 54% of the waves' cycles) one workgroup a CU does not cover (vector
+// unit 50, 50, 39%, matrix unit 7, 12, 14%).
+// One sequence of 700 tokens: 8.8 us of dependent reads (lengths, page, K, the
+// weights before).
 // ---------------------------------------------------------------------------
 constexpr int kWeighRun = 512;
 
@@ -310,7 +315,10 @@ weigh_rows_kernel(WeighArgs w)
 // and a tile's exponentials stand between the products of the next.
 //
 // A prompt of 4096, 32/8 heads of 128: 102 us and 5.4 for the joining launch, 0.68
-// PFLOP/s.  Graphs of both launches replayed, 123 us so: with 64 tokens a wave 147
+// PFLOP/s.  The matrix unit works 36% of the cycles and the vector unit 57%, in all
+// 94%: hardly any of either runs beside the other (the waves of a workgroup pass
+// the barrier of each 32 rows together).  Graphs of both launches replayed, 123 us
+// so: with 64 tokens a wave 147
 // (two waves on a SIMD, products and exponentials in turn), 129 (exponentials
 // between the products), 127 (those and one tile ahead); three waves of 32 tokens
 // 118-125 (registers spill; D = 256 143 for 109); tokens as rows of the product
